@@ -32,7 +32,12 @@ EXPORTED = ("bd_attn_fwd", "bd_attn_decode", "bd_attn_decode_workspace_bytes",
             "bd_attn_get_device_status", "bd_attn_status_string",
             "bd_spec_accept", "bd_cache_append", "bd_cache_crop",
             "bd_sprint_prune", "bd_sprint_workspace_bytes", "bd_attn_bwd",
-            "bd_attn_bwd_workspace_bytes")
+            "bd_attn_bwd_workspace_bytes", "bd_rope_table", "bd_rope",
+            "bd_cache_append_q8", "bd_cache_read_q8", "bd_attn_decode_q8",
+            "bd_spec_verify")
+
+# scalings of rope_table
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class BdAttnError(RuntimeError):
@@ -84,6 +89,19 @@ def load(path: str = LIB_PATH):
                                     ctypes.c_size_t]
     lib.bd_sprint_workspace_bytes.restype = ctypes.c_size_t
     lib.bd_sprint_workspace_bytes.argtypes = [i, i]
+    dbl, sz = ctypes.c_double, ctypes.c_size_t
+    lib.bd_rope_table.restype = i
+    lib.bd_rope_table.argtypes = [vp, vp, i, dbl, i, dbl, i, dbl, dbl]
+    lib.bd_rope.restype = i
+    lib.bd_rope.argtypes = [vp] * 7 + [i] * 8 + [f, i, vp]
+    lib.bd_cache_append_q8.restype = i
+    lib.bd_cache_append_q8.argtypes = [vp] * 8 + [i] * 7 + [vp]
+    lib.bd_cache_read_q8.restype = i
+    lib.bd_cache_read_q8.argtypes = [vp] * 7 + [i] * 5 + [vp]
+    lib.bd_attn_decode_q8.restype = i
+    lib.bd_attn_decode_q8.argtypes = [vp] * 8 + [i] * 6 + [vp, i, i, vp, sz]
+    lib.bd_spec_verify.restype = i
+    lib.bd_spec_verify.argtypes = [vp] * 8 + [i] * 3 + [vp]
     _lib = lib
     return lib
 
@@ -153,6 +171,50 @@ def bd_sprint_prune(k_cache, v_cache, cache_len, conf, modality, alpha,
 
 def bd_sprint_workspace_bytes(B, S_cap):
     return int(load().bd_sprint_workspace_bytes(B, S_cap))
+
+
+def bd_rope_table(inv_freq, mscale, rot_dim, base, scaling, factor,
+                  trained_len, beta_fast, beta_slow):
+    return load().bd_rope_table(inv_freq, mscale, rot_dim, base, scaling,
+                                factor, trained_len, beta_fast, beta_slow)
+
+
+def bd_rope(q, k, q_out, k_out, inv_freq, start, positions, B, Hq, Hkv, N, d,
+            rot_dim, period, interleaved, mscale, adjoint, stream):
+    return load().bd_rope(q, k, q_out, k_out, inv_freq, start, positions, B,
+                          Hq, Hkv, N, d, rot_dim, period, interleaved, mscale,
+                          adjoint, stream)
+
+
+def bd_cache_append_q8(k_cache, v_cache, k_scale, v_scale, cache_len, k_new,
+                       v_new, n_new, B, Hkv, b, d, S_cap, group, advance,
+                       stream):
+    return load().bd_cache_append_q8(k_cache, v_cache, k_scale, v_scale,
+                                     cache_len, k_new, v_new, n_new, B, Hkv,
+                                     b, d, S_cap, group, advance, stream)
+
+
+def bd_cache_read_q8(k_cache, v_cache, k_scale, v_scale, cache_len, k_out,
+                     v_out, B, Hkv, d, S_cap, group, stream):
+    return load().bd_cache_read_q8(k_cache, v_cache, k_scale, v_scale,
+                                   cache_len, k_out, v_out, B, Hkv, d, S_cap,
+                                   group, stream)
+
+
+def bd_attn_decode_q8(q_blk, k_cache, v_cache, k_scale, v_scale, cache_len,
+                      out, lse, B, Hq, Hkv, b, d, intra_block_mode, stream,
+                      S_cap, group, workspace, workspace_bytes):
+    return load().bd_attn_decode_q8(q_blk, k_cache, v_cache, k_scale, v_scale,
+                                    cache_len, out, lse, B, Hq, Hkv, b, d,
+                                    intra_block_mode, stream, S_cap, group,
+                                    workspace, workspace_bytes)
+
+
+def bd_spec_verify(draft, draft_prob, target_prob, u_accept, u_sample,
+                   n_draft, n_accept, next_token, B, b, V, stream):
+    return load().bd_spec_verify(draft, draft_prob, target_prob, u_accept,
+                                 u_sample, n_draft, n_accept, next_token, B,
+                                 b, V, stream)
 
 
 def bd_attn_debug_inject_fault(kind):
@@ -398,6 +460,260 @@ def sprint_prune(k_cache, v_cache, cache_len, conf, modality, alpha=0.5,
     if st != BD_OK:
         raise BdAttnError(st, "bd_sprint_prune")
     return k_out, v_out, kept, new_len, score
+
+
+# ---------------------------------------------------------------------------
+# the serving step over a KV cache in 8 bits
+
+
+def _check_on(t, dtype, shape, device, what):
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and t.device == device):
+        raise ValueError("%s must be a contiguous %s tensor on %s" %
+                         (what, dtype, device))
+    if t.shape != shape:
+        raise ValueError("%s must have the shape %s" % (what, tuple(shape)))
+
+
+class _on:
+    """Makes `device` current for a call if it is not (a launch goes to the
+    current device)."""
+
+    def __init__(self, device):
+        import torch
+        self.guard = (None if device.index == torch.cuda.current_device()
+                      else torch.cuda.device(device))
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
+               factor: float = 1.0, trained_len: int = 0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0,
+               device="cuda"):
+    """Frequencies of rotary positions: (inv_freq [rot_dim / 2] fp64 on
+    ``device``, mscale).  ``scaling``: "plain", "linear" (positions divided by
+    ``factor``), "ntk" (a larger base) or "yarn" (slow pairs divided by
+    ``factor``, pairs that turn more than ``beta_fast`` times over
+    ``trained_len`` kept, and an attention factor ``mscale``)."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % sorted(ROPE_SCALINGS))
+    inv_freq = torch.empty(max(1, int(rot_dim) // 2), dtype=torch.float64)
+    mscale = ctypes.c_float()
+    st = bd_rope_table(inv_freq.data_ptr(), ctypes.addressof(mscale),
+                       int(rot_dim), float(base), ROPE_SCALINGS[scaling],
+                       float(factor), int(trained_len), float(beta_fast),
+                       float(beta_slow))
+    if st != BD_OK:
+        raise BdAttnError(st, "bd_rope_table")
+    return inv_freq.to(device), mscale.value
+
+
+def rope(q, k, inv_freq, start=None, positions=None, period: int | None = None,
+         interleaved: bool = False, mscale: float = 1.0,
+         adjoint: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [B,Hq,N,d] and k [B,Hkv,N,d] (or None), bf16 CUDA.
+
+    Row r of sequence i stands at ``positions[i, r]`` (int32 [B,N]) or at
+    ``start[i] + r % period`` (start int32 [B], None: 0; period None: N).  The
+    first 2 * len(inv_freq) dims turn, ``inv_freq`` and ``mscale`` as from
+    ``rope_table``.  ``adjoint`` maps gradients of the outputs to those of the
+    inputs.  q_out may be q and k_out may be k.  Returns (q_out, k_out)."""
+    import torch
+    B, Hq, N, d = q.shape
+    dev = q.device
+    bf = torch.bfloat16
+    _check_on(q, bf, q.shape, dev, "q")
+    Hkv = 0
+    if k is not None:
+        Hkv = k.shape[1]
+        _check_on(k, bf, (B, Hkv, N, d), dev, "k")
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        else:
+            _check_on(k_out, bf, k.shape, dev, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    else:
+        _check_on(q_out, bf, q.shape, dev, "q_out")
+    _check_on(inv_freq, torch.float64, (inv_freq.numel(),), dev, "inv_freq")
+    if start is not None:
+        _check_on(start, torch.int32, (B,), dev, "start")
+    if positions is not None:
+        _check_on(positions, torch.int32, (B, N), dev, "positions")
+    with _on(dev):
+        st = load().bd_rope(
+            q.data_ptr(), None if k is None else k.data_ptr(),
+            q_out.data_ptr(), None if k is None else k_out.data_ptr(),
+            inv_freq.data_ptr(), None if start is None else start.data_ptr(),
+            None if positions is None else positions.data_ptr(), B, Hq, Hkv, N,
+            d, 2 * inv_freq.numel(), N if period is None else period,
+            int(interleaved), mscale, int(adjoint), _stream_handle(stream))
+    if st != BD_OK:
+        raise BdAttnError(st, "bd_rope")
+    return q_out, k_out
+
+
+def _check_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group):
+    import torch
+    B, Hkv, S_cap, d = shape = k_cache.shape
+    dev = k_cache.device
+    if group not in (16, 32, 64, 128):
+        raise ValueError("group must be 16, 32, 64 or 128")
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    _check_on(k_cache, e4m3, shape, dev, "k_cache")
+    _check_on(v_cache, e4m3, shape, dev, "v_cache")
+    groups = (B, Hkv, -(-S_cap // group))
+    _check_on(k_scale, f32, groups, dev, "k_scale")
+    _check_on(v_scale, f32, groups, dev, "v_scale")
+    _check_on(cache_len, torch.int32, (B,), dev, "cache_len")
+    return dev
+
+
+def cache_append_q8(k_cache, v_cache, k_scale, v_scale, cache_len, k_new,
+                    v_new, group: int, n_new=None, advance: bool = True,
+                    stream=None):
+    """Quantise rows 0..n_new[i]-1 (None: all) of k_new/v_new [B,Hkv,b,d] bf16
+    into the cache in 8 bits (e4m3 codes [B,Hkv,S_cap,d] and fp32 scales
+    [B,Hkv,ceil(S_cap/group)]) behind its cache_len[i] rows, in place, and
+    advance cache_len.  ``advance=False``: the rows are a draft, to be attended
+    to and overwritten.  k_new = v_new = None with n_new: the rows are there
+    already, only the lengths advance."""
+    import torch
+    dev = _check_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group)
+    B, Hkv, S_cap, d = k_cache.shape
+    kp = vp = None
+    if k_new is None and v_new is None:
+        if n_new is None:
+            raise ValueError("nothing to append: neither rows nor n_new")
+        b = S_cap
+    else:
+        if k_new is None or v_new is None:
+            raise ValueError("k_new and v_new must be given together")
+        b = k_new.shape[2]
+        _check_on(k_new, torch.bfloat16, (B, Hkv, b, d), dev, "k_new")
+        _check_on(v_new, torch.bfloat16, (B, Hkv, b, d), dev, "v_new")
+        kp, vp = k_new.data_ptr(), v_new.data_ptr()
+    if n_new is not None:
+        _check_on(n_new, torch.int32, (B,), dev, "n_new")
+    with _on(dev):
+        st = load().bd_cache_append_q8(
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), cache_len.data_ptr(), kp, vp,
+            None if n_new is None else n_new.data_ptr(), B, Hkv, b, d, S_cap,
+            group, int(advance), _stream_handle(stream))
+    if st != BD_OK:
+        raise BdAttnError(st, "bd_cache_append_q8")
+
+
+def cache_read_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group: int,
+                  k_out=None, v_out=None, stream=None):
+    """Rows 0..cache_len[i]-1 of the cache in 8 bits as bf16.  Returns (k_out,
+    v_out) [B,Hkv,S_cap,d]; later rows are left as they are (0 in outputs that
+    are made here)."""
+    import torch
+    dev = _check_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group)
+    B, Hkv, S_cap, d = shape = k_cache.shape
+    outs = []
+    for t, w in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _check_on(t, torch.bfloat16, shape, dev, w)
+        outs.append(t)
+    k_out, v_out = outs
+    with _on(dev):
+        st = load().bd_cache_read_q8(
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), cache_len.data_ptr(), k_out.data_ptr(),
+            v_out.data_ptr(), B, Hkv, d, S_cap, group, _stream_handle(stream))
+    if st != BD_OK:
+        raise BdAttnError(st, "bd_cache_read_q8")
+    return k_out, v_out
+
+
+def decode_q8(q_blk, k_cache, v_cache, k_scale, v_scale, cache_len, mode: int,
+              group: int, out=None, lse=None, workspace=None, stream=None):
+    """``decode`` over the cache in 8 bits of ``cache_append_q8``: same masks,
+    modes, outputs and workspace.  Returns (out, lse)."""
+    import torch
+    dev = _check_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group)
+    B, Hq, b, d = q_blk.shape
+    Hkv, S_cap = k_cache.shape[1], k_cache.shape[2]
+    if k_cache.shape[0] != B or k_cache.shape[3] != d:
+        raise ValueError("shape mismatch")
+    _check_on(q_blk, torch.bfloat16, q_blk.shape, dev, "q_blk")
+    if out is None:
+        out = torch.empty_like(q_blk)
+    else:
+        _check_on(out, torch.bfloat16, q_blk.shape, dev, "out")
+    if lse is None:
+        lse = torch.empty((B, Hq, b), device=dev, dtype=torch.float32)
+    else:
+        _check_on(lse, torch.float32, (B, Hq, b), dev, "lse")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on %s" % dev)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    with _on(dev):
+        st = load().bd_attn_decode_q8(
+            q_blk.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), cache_len.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, b, d, mode,
+            _stream_handle(stream), S_cap, group, ws_ptr, ws_bytes)
+    if st != BD_OK:
+        raise BdAttnError(st, "bd_attn_decode_q8")
+    return out, lse
+
+
+def spec_verify(draft, draft_prob, target_prob, u_accept, u_sample,
+                n_draft=None, n_accept=None, next_token=None, stream=None):
+    """Accept a prefix of draft [B,b] int32 by speculative sampling and draw
+    the token behind it: draft_prob [B,b,V] fp32 (None: the draft was not
+    sampled), target_prob [B,b+1,V] fp32, random numbers u_accept [B,b] and
+    u_sample [B] fp32 in [0,1), n_draft [B] int32 (None: b).  Returns
+    (n_accept [B], next_token [B]) int32 on the device."""
+    import torch
+    B, b = draft.shape
+    V = target_prob.shape[-1]
+    dev = draft.device
+    i32, f32 = torch.int32, torch.float32
+    _check_on(draft, i32, (B, b), dev, "draft")
+    _check_on(target_prob, f32, (B, b + 1, V), dev, "target_prob")
+    _check_on(u_accept, f32, (B, b), dev, "u_accept")
+    _check_on(u_sample, f32, (B,), dev, "u_sample")
+    if draft_prob is not None:
+        _check_on(draft_prob, f32, (B, b, V), dev, "draft_prob")
+    if n_draft is not None:
+        _check_on(n_draft, i32, (B,), dev, "n_draft")
+    if n_accept is None:
+        n_accept = torch.empty(B, dtype=i32, device=dev)
+    else:
+        _check_on(n_accept, i32, (B,), dev, "n_accept")
+    if next_token is None:
+        next_token = torch.empty(B, dtype=i32, device=dev)
+    else:
+        _check_on(next_token, i32, (B,), dev, "next_token")
+    with _on(dev):
+        st = load().bd_spec_verify(
+            draft.data_ptr(), None if draft_prob is None else draft_prob.data_ptr(),
+            target_prob.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+            None if n_draft is None else n_draft.data_ptr(),
+            n_accept.data_ptr(), next_token.data_ptr(), B, b, V,
+            _stream_handle(stream))
+    if st != BD_OK:
+        raise BdAttnError(st, "bd_spec_verify")
+    return n_accept, next_token
 
 
 def workspace_bytes(B, Hq, Hkv, b, d, S_cap) -> int:

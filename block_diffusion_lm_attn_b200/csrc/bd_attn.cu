@@ -6,12 +6,15 @@
 // columns): the forward on the paired kernel (attn_tc_pair.cuh) when the GQA
 // group is even, else on the one-tile persistent kernel (attn_tc_persist.cuh),
 // which also runs block decode; the backward in attn_tc_bwd.cuh; the cache
-// and SPRINT kernels in cache_ops.cuh.
+// and SPRINT kernels in cache_ops.cuh.  The serving step over a cache in 8
+// bits: rope.cuh (positions), cache_q8.cuh (writing and reading the cache),
+// attn_q8.cuh (decode), spec_verify.cuh (verification).
 #include "bd_attn.h"
 #include "bd_attn_debug.h"
 
 #include <cmath>
 #include <cstdint>
+#include <climits>
 #include <cstdlib>
 #include <algorithm>
 #include <atomic>
@@ -24,8 +27,12 @@
 #include "attn_tc_persist.cuh"
 #include "attn_tc_pair.cuh"
 #include "attn_tc_bwd.cuh"
+#include "attn_q8.cuh"
 #include "bd_common.cuh"
 #include "cache_ops.cuh"
+#include "cache_q8.cuh"
+#include "rope.cuh"
+#include "spec_verify.cuh"
 
 namespace {
 
@@ -365,6 +372,37 @@ bd_status decode_launch(const void *q_blk, const void *k_cache,
     }
 }
 
+
+inline bool aligned4(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
+// Group sizes of a cache in 8 bits: whole 16-key chunks of a key tile.
+inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
+
+// Host-side checks shared by the calls on a cache in 8 bits.
+bd_status q8_cache_validate(const void *k_cache, const void *v_cache, const float *k_scale,
+                            const float *v_scale, const int32_t *cache_len, int B, int Hkv,
+                            int d, int S_cap, int group)
+{
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !cache_len)
+        return BD_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scale) ||
+        !aligned4(v_scale) || !aligned4(cache_len))
+        return BD_ERR_INVALID_ARG;
+    if (k_cache == v_cache || k_scale == v_scale)
+        return BD_ERR_INVALID_ARG;
+    if (B <= 0 || Hkv <= 0 || d <= 0 || S_cap <= 0 || group <= 0)
+        return BD_ERR_INVALID_ARG;
+    if (!supported_d(d) || !supported_group(group))
+        return BD_ERR_UNSUPPORTED;
+    // grid limits, and positions that stay in 32 bits when rounded up
+    if (B > 65535 || Hkv > 32767 || S_cap > (1 << 30))
+        return BD_ERR_UNSUPPORTED;
+    return BD_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -670,6 +708,235 @@ bd_status bd_sprint_prune(const void *k_cache, const void *v_cache,
     bd::bd_sprint_compact_kernel<<<dim3((S_cap + 7) / 8, B), 256, 0, stream>>>(
         static_cast<const bf16 *>(k_cache), static_cast<const bf16 *>(v_cache), kept, new_len,
         static_cast<bf16 *>(k_out), static_cast<bf16 *>(v_out), Hkv, d, S_cap);
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
+bd_status bd_rope_table(double *inv_freq, float *mscale, int rot_dim, double base,
+                        int scaling, double factor, int trained_len, double beta_fast,
+                        double beta_slow)
+{
+    if (!inv_freq || !mscale || rot_dim <= 0 || rot_dim % 2 != 0)
+        return BD_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !std::isfinite(base) || scaling < 0 || scaling > 3)
+        return BD_ERR_INVALID_ARG;
+    if (scaling != BD_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return BD_ERR_INVALID_ARG;
+    if (scaling == BD_ROPE_NTK && rot_dim <= 2)
+        return BD_ERR_INVALID_ARG;
+    if (scaling == BD_ROPE_YARN &&
+        (trained_len <= 0 || !(beta_slow >= 0.0) || !(beta_fast > beta_slow) ||
+         !std::isfinite(beta_fast)))
+        return BD_ERR_INVALID_ARG;
+    if (scaling == BD_ROPE_NTK)
+        base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        double g = f;
+        if (scaling == BD_ROPE_LINEAR)
+            g = f / factor;
+        if (scaling == BD_ROPE_YARN) {
+            const double turns = trained_len * f / (2.0 * M_PI);
+            const double keep = std::min(1.0, std::max(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+            g = f / factor * (1.0 - keep) + f * keep;
+        }
+        inv_freq[i] = g;
+    }
+    *mscale = scaling == BD_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return BD_OK;
+}
+
+bd_status bd_rope(const void *q, const void *k, void *q_out, void *k_out,
+                  const double *inv_freq, const int32_t *start,
+                  const int32_t *positions, int B, int Hq, int Hkv, int N, int d,
+                  int rot_dim, int period, int interleaved, float mscale,
+                  int adjoint, cudaStream_t stream)
+{
+    if (!q || !q_out || (!k != !k_out) || !inv_freq || (start && positions))
+        return BD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) ||
+        (reinterpret_cast<uintptr_t>(inv_freq) & 7u) || !aligned4(start) || !aligned4(positions))
+        return BD_ERR_INVALID_ARG;
+    if (B <= 0 || Hq <= 0 || N <= 0 || d <= 0 || period <= 0 || (k ? Hkv <= 0 : Hkv != 0))
+        return BD_ERR_INVALID_ARG;
+    if (rot_dim <= 0 || rot_dim > d || !std::isfinite(mscale) ||
+        (interleaved != 0 && interleaved != 1) || (adjoint != 0 && adjoint != 1))
+        return BD_ERR_INVALID_ARG;
+    // two outputs in one buffer, or an output over the other input
+    if (k && (q_out == k_out || q_out == k || k_out == q))
+        return BD_ERR_INVALID_ARG;
+    if (!supported_d(d) || rot_dim % 16 != 0)
+        return BD_ERR_UNSUPPORTED;
+    const int rows_cta = bd::kRopeThreads / (d / 16);
+    const long long tiles = (long long)B * cdiv(N, rows_cta);
+    if (tiles > 0x7fffffffLL || (long long)Hq + Hkv > 0x7fffffffLL)
+        return BD_ERR_UNSUPPORTED;
+
+    bd::RopeParams p = {};
+    p.q = static_cast<const bf16 *>(q);
+    p.k = static_cast<const bf16 *>(k);
+    p.q_out = static_cast<bf16 *>(q_out);
+    p.k_out = static_cast<bf16 *>(k_out);
+    p.inv_freq = inv_freq;
+    p.start = start;
+    p.positions = positions;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.N = N; p.d = d;
+    p.rot = rot_dim; p.period = period;
+    p.copy = q_out != q || k_out != k;
+    p.mscale = mscale;
+    p.sign = adjoint ? -1.f : 1.f;
+    // as many heads a CTA as still leave a few CTAs to every SM
+    const long long heads = (long long)Hq + Hkv;
+    const long long groups = std::min(std::min(heads, 65535LL), std::max(1LL, cdiv(8LL * kMaxGrid, tiles)));
+    p.heads = (int)cdiv(heads, groups);
+    const dim3 grid((unsigned)tiles, (unsigned)cdiv(heads, p.heads));
+    if (interleaved)
+        bd::bd_rope_kernel<true><<<grid, bd::kRopeThreads, 0, stream>>>(p);
+    else
+        bd::bd_rope_kernel<false><<<grid, bd::kRopeThreads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
+bd_status bd_cache_append_q8(void *k_cache, void *v_cache, float *k_scale,
+                             float *v_scale, int32_t *cache_len, const void *k_new,
+                             const void *v_new, const int32_t *n_new, int B,
+                             int Hkv, int b, int d, int S_cap, int group,
+                             int advance, cudaStream_t stream)
+{
+    const bd_status st = q8_cache_validate(k_cache, v_cache, k_scale, v_scale, cache_len, B,
+                                           Hkv, d, S_cap, group);
+    if (st != BD_OK && st != BD_ERR_UNSUPPORTED)
+        return st;
+    if ((!k_new != !v_new) || b <= 0 || (advance != 0 && advance != 1) ||
+        (!k_new && !advance) || !aligned16(k_new) || !aligned16(v_new) || !aligned4(n_new))
+        return BD_ERR_INVALID_ARG;
+    if (st != BD_OK || b > (1 << 30))
+        return BD_ERR_UNSUPPORTED;
+    bd::Q8Params p = {};
+    p.k_cache = static_cast<uint8_t *>(k_cache);
+    p.v_cache = static_cast<uint8_t *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.cache_len = cache_len;
+    p.n_new = n_new;
+    p.k_new = static_cast<const bf16 *>(k_new);
+    p.v_new = static_cast<const bf16 *>(v_new);
+    p.B = B; p.Hkv = Hkv; p.b = b; p.d = d; p.S_cap = S_cap; p.T = group;
+    p.groups = (int)cdiv(S_cap, group);
+    if (k_new) {
+        // the first group may hold older rows: one group more than b rows fill
+        const unsigned touched = (unsigned)std::min<long long>(cdiv(b, group) + 1, p.groups);
+        const dim3 grid(touched, 2 * Hkv, B);
+        const int vec = group * d / 8;
+        const int threads = std::min(bd::kQ8Threads, vec);
+        switch ((vec + threads - 1) / threads) {
+        case 1: bd::bd_cache_append_q8_kernel<1><<<grid, threads, 0, stream>>>(p); break;
+        case 2: bd::bd_cache_append_q8_kernel<2><<<grid, threads, 0, stream>>>(p); break;
+        case 4: bd::bd_cache_append_q8_kernel<4><<<grid, threads, 0, stream>>>(p); break;
+        default: bd::bd_cache_append_q8_kernel<8><<<grid, threads, 0, stream>>>(p); break;
+        }
+        if (cudaGetLastError() != cudaSuccess)
+            return BD_ERR_CUDA;
+    }
+    if (advance) {
+        bd::bd_cache_advance_kernel<<<(B + 255) / 256, 256, 0, stream>>>(p, k_new ? 0 : 1);
+        if (cudaGetLastError() != cudaSuccess)
+            return BD_ERR_CUDA;
+    }
+    return BD_OK;
+}
+
+bd_status bd_cache_read_q8(const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale,
+                           const int32_t *cache_len, void *k_out, void *v_out, int B,
+                           int Hkv, int d, int S_cap, int group, cudaStream_t stream)
+{
+    const bd_status st = q8_cache_validate(k_cache, v_cache, k_scale, v_scale, cache_len, B,
+                                           Hkv, d, S_cap, group);
+    if (st != BD_OK && st != BD_ERR_UNSUPPORTED)
+        return st;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || k_out == v_out ||
+        k_out == k_cache || k_out == v_cache || v_out == k_cache || v_out == v_cache)
+        return BD_ERR_INVALID_ARG;
+    if (st != BD_OK)
+        return st;
+    bd::Q8Params p = {};
+    p.k_cache = static_cast<uint8_t *>(const_cast<void *>(k_cache));
+    p.v_cache = static_cast<uint8_t *>(const_cast<void *>(v_cache));
+    p.k_scale = const_cast<float *>(k_scale);
+    p.v_scale = const_cast<float *>(v_scale);
+    p.cache_len = const_cast<int32_t *>(cache_len);
+    p.k_out = static_cast<bf16 *>(k_out);
+    p.v_out = static_cast<bf16 *>(v_out);
+    p.B = B; p.Hkv = Hkv; p.d = d; p.S_cap = S_cap; p.T = group;
+    p.groups = (int)cdiv(S_cap, group);
+    const dim3 grid((unsigned)cdiv((long long)S_cap * d / 16, bd::kQ8Threads), 2 * Hkv, B);
+    bd::bd_cache_read_q8_kernel<<<grid, bd::kQ8Threads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
+bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache, const void *v_cache,
+                            const float *k_scale, const float *v_scale,
+                            const int32_t *cache_len, void *out, float *lse, int B,
+                            int Hq, int Hkv, int b, int d, int intra_block_mode,
+                            cudaStream_t stream, int S_cap, int group,
+                            void *workspace, size_t workspace_bytes)
+{
+    DecodePlan pl;
+    bd_status st = decode_validate(q_blk, k_cache, v_cache, cache_len, out, lse, B, Hq, Hkv,
+                                   b, d, intra_block_mode, S_cap, pl);
+    if (st != BD_OK && st != BD_ERR_UNSUPPORTED)
+        return st;
+    const bd_status sq = q8_cache_validate(k_cache, v_cache, k_scale, v_scale, cache_len, B,
+                                           Hkv, d, S_cap, group);
+    if (sq != BD_OK || st != BD_OK)
+        return sq == BD_ERR_INVALID_ARG ? sq : BD_ERR_UNSUPPORTED;
+    if (workspace) {
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < pl.total_bytes)
+            return BD_ERR_INVALID_ARG;
+    }
+    bd::Q8Attn p = {};
+    p.q = static_cast<const bf16 *>(q_blk);
+    p.k = static_cast<const uint8_t *>(k_cache);
+    p.v = static_cast<const uint8_t *>(v_cache);
+    p.ks = k_scale;
+    p.vs = v_scale;
+    p.cache_len = cache_len;
+    p.out = static_cast<bf16 *>(out);
+    p.lse = lse;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.b = b; p.d = d; p.S_cap = S_cap;
+    p.T = group; p.groups = (int)cdiv(S_cap, group); p.mode = intra_block_mode;
+    p.scale_log2 = (1.0f / std::sqrt((float)d)) * bd::kLog2e;
+    const unsigned grid = (unsigned)cdiv((long long)B * Hq * b, 4);
+    if (d == 128)
+        bd::bd_decode_q8_simt_kernel<128><<<grid, 128, 0, stream>>>(p);
+    else if (d == 64)
+        bd::bd_decode_q8_simt_kernel<64><<<grid, 128, 0, stream>>>(p);
+    else
+        bd::bd_decode_q8_simt_kernel<32><<<grid, 128, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
+bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
+                         const float *target_prob, const float *u_accept,
+                         const float *u_sample, const int32_t *n_draft,
+                         int32_t *n_accept, int32_t *next_token, int B, int b,
+                         int V, cudaStream_t stream)
+{
+    if (!draft || !target_prob || !u_accept || !u_sample || !n_accept || !next_token ||
+        n_accept == next_token)
+        return BD_ERR_INVALID_ARG;
+    if (!aligned4(draft) || !aligned4(draft_prob) || !aligned4(target_prob) ||
+        !aligned4(u_accept) || !aligned4(u_sample) || !aligned4(n_draft) ||
+        !aligned4(n_accept) || !aligned4(next_token))
+        return BD_ERR_INVALID_ARG;
+    if (B <= 0 || b <= 0 || V <= 0)
+        return BD_ERR_INVALID_ARG;
+    if (V > bd::kVerifyMaxVocab)
+        return BD_ERR_UNSUPPORTED;
+    bd::VerifyParams p = {draft, draft_prob, target_prob, u_accept, u_sample, n_draft,
+                          n_accept, next_token, B, b, V};
+    const int smem = (int)cdiv(V, bd::kVerifySeg) * (int)sizeof(double);
+    bd::bd_spec_verify_kernel<<<B, bd::kVerifyThreads, smem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 

@@ -357,6 +357,200 @@ BD_API bd_status bd_sprint_prune(const void *k_cache, const void *v_cache,
 /* Bytes of scratch bd_sprint_prune needs (0 on bad sizes).  Host only. */
 BD_API size_t bd_sprint_workspace_bytes(int B, int S_cap);
 
+/*
+ * The serving step over a KV cache in 8 bits.
+ *
+ * The pages decode over a cache in the model's own type; the calls below have
+ * no counterpart on them.  They are the operators that a step of block
+ * decoding (bd_attn_decode) is made of when the cache is held in 8 bits:
+ * rotary positions, quantising rows as they are written, attention over the
+ * codes, verification by sampling.  bd_cache_crop works on such a cache as it
+ * is; for bd_sprint_prune read the prefix back, prune it and append the kept
+ * rows to an emptied cache.
+ *
+ * The cache in 8 bits
+ *   k_cache, v_cache  [B, Hkv, S_cap, d] e4m3 codes (1 sign, 4 exponent, 3
+ *                     mantissa bits, no infinity, largest value 448)
+ *   k_scale, v_scale  [B, Hkv, ceil(S_cap / group)] fp32: one scale for every
+ *                     `group` consecutive positions of a kv-head; a position's
+ *                     values are its codes times its group's scale
+ *   group             16, 32, 64 or 128
+ * bd_cache_append_q8 writes powers of two between 2^-64 and 2^120 as scales.
+ * The reading calls take any positive finite scale in the groups that hold
+ * visible positions; codes and scales behind them are never used, whatever
+ * they hold.
+ */
+
+/* Scalings of bd_rope_table. */
+#define BD_ROPE_PLAIN 0
+#define BD_ROPE_LINEAR 1
+#define BD_ROPE_NTK 2
+#define BD_ROPE_YARN 3
+
+/*
+ * Frequencies of rotary positions (host arithmetic; needs no GPU).
+ *
+ * f_i = base^(-2 i / rot_dim) radians a position for pair i, and for contexts
+ * `factor` times longer than the trained one:
+ *   BD_ROPE_LINEAR  f_i / factor (position interpolation);
+ *   BD_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) for base;
+ *   BD_ROPE_YARN    f_i / factor (1 - w) + f_i w with w = (turns - beta_slow) /
+ *                   (beta_fast - beta_slow) clamped to [0, 1], turns =
+ *                   trained_len f_i / 2 pi (the "NTK-by-parts" rule of Peng et
+ *                   al., "YaRN", section 3.2), and mscale = 0.1 ln(factor) + 1.
+ *
+ *   inv_freq  [rot_dim / 2] fp64, HOST memory (written)
+ *   mscale    HOST memory (written): 1 but for BD_ROPE_YARN
+ *
+ * Errors: BD_ERR_INVALID_ARG for a null pointer, rot_dim <= 0 or odd (<= 2
+ * with BD_ROPE_NTK), base not above 1 and finite, an unknown scaling, factor
+ * not in [1, inf) where it is used, and for BD_ROPE_YARN trained_len <= 0 or
+ * not 0 <= beta_slow < beta_fast < inf.
+ */
+BD_API bd_status bd_rope_table(double *inv_freq, float *mscale, int rot_dim,
+                               double base, int scaling, double factor,
+                               int trained_len, double beta_fast, double beta_slow);
+
+/*
+ * Rotary positions of queries and keys, or the gradient through them.
+ *
+ * Row r of sequence i has the position positions[i][r], or start[i] + r mod
+ * period (start NULL: 0).  The training form's [x_t ; x_0] has N = 2L and
+ * period = L: a noisy token stands where its clean one does.  A decoded block
+ * has N = period = b and start = cache_len.  With t = position * inv_freq[j],
+ * the pair (x_a, x_b) of every head becomes
+ *     (mscale (x_a cos t - x_b sin t), mscale (x_b cos t + x_a sin t)),
+ * (a, b) = (j, j + rot_dim/2), or (2j, 2j + 1) if interleaved; dims from
+ * rot_dim on are copied.  adjoint = 1 takes -t: it maps the gradients of
+ * q_out and k_out to those of q and k (with mscale 1 it is the inverse).
+ * Angles are reduced in fp64, so positions may be as large as int32 holds.
+ *
+ *   q, q_out   [B, Hq,  N, d] bf16   (read, written)
+ *   k, k_out   [B, Hkv, N, d] bf16   (both NULL with Hkv = 0: queries alone)
+ *              q_out may be q, and k_out may be k; no other overlap
+ *   inv_freq   [rot_dim / 2] fp64, DEVICE
+ *   start      [B] int32, DEVICE, or NULL
+ *   positions  [B, N] int32, DEVICE, or NULL; not together with start
+ *
+ * Errors: BD_ERR_INVALID_ARG for a null (other than the above) or misaligned
+ * pointer, a size or period <= 0, rot_dim > d, a non-finite mscale, flags not
+ * 0/1, or aliased outputs; BD_ERR_UNSUPPORTED for d not in {32, 64, 128} or
+ * rot_dim not a multiple of 16; BD_ERR_CUDA if the launch fails.
+ */
+BD_API bd_status bd_rope(const void *q, const void *k, void *q_out, void *k_out,
+                         const double *inv_freq, const int32_t *start,
+                         const int32_t *positions, int B, int Hq, int Hkv,
+                         int N, int d, int rot_dim, int period,
+                         int interleaved, float mscale, int adjoint,
+                         struct CUstream_st *stream);
+
+/*
+ * Quantise rows into the cache in 8 bits at its tail.
+ *
+ * Rows 0 .. n_new[i]-1 of k_new, v_new go to positions cache_len[i] ..
+ * cache_len[i]+n_new[i]-1.  Every group that takes a row gets the scale s =
+ * 2^max(-64, k), k the smallest with |x| <= 448 * 2^k over the finite values
+ * of the rows that it then holds (the new ones, and those below cache_len[i]),
+ * and all of those rows the codes rne(x / s): +-inf becomes +-448, NaN stays
+ * NaN.  Rows that stay are requantised from their values, which is exact
+ * unless they fall below the smallest code, 2^-9 s.  Positions from
+ * cache_len[i]+n_new[i] on keep their codes, and groups that take no row keep
+ * their scales; positions behind the rows in a written group lose their value.
+ *
+ *   cache_len      [B] int32, DEVICE (read; advanced by n_new[i] if advance)
+ *   k_new, v_new   [B, Hkv, b, d] bf16 (read).  Both NULL, with advance = 1:
+ *                  the rows are already there, only the length advances.
+ *   n_new          [B] int32, DEVICE (read), or NULL: b rows each
+ *   advance        0: the rows are a draft behind the prefix, to be attended
+ *                  to (modes 0 and 1 of bd_attn_decode_q8) and overwritten;
+ *                  1: they join the prefix
+ *
+ * One kernel, and one more to advance.  Nothing is allocated; the call can be
+ * captured in a CUDA graph.  A sequence with n_new[i] outside [0, b], a
+ * negative length or cache_len[i] + n_new[i] > S_cap is left untouched and the
+ * device status word records BD_ERR_DEVICE_TIMEOUT.
+ * Errors: BD_ERR_INVALID_ARG for a null or misaligned pointer (16 bytes for
+ * codes and rows, 4 for the rest), codes or scales of K and V in one buffer, a
+ * size <= 0, only one of k_new and v_new, or nothing to do;
+ * BD_ERR_UNSUPPORTED for d not in {32, 64, 128}, another group, B > 65535,
+ * Hkv > 32767 or S_cap or b > 2^30; BD_ERR_CUDA if a launch fails.
+ */
+BD_API bd_status bd_cache_append_q8(void *k_cache, void *v_cache, float *k_scale,
+                                    float *v_scale, int32_t *cache_len,
+                                    const void *k_new, const void *v_new,
+                                    const int32_t *n_new, int B, int Hkv, int b,
+                                    int d, int S_cap, int group, int advance,
+                                    struct CUstream_st *stream);
+
+/*
+ * Read the cache in 8 bits back: rows 0 .. cache_len[i]-1 of k_out, v_out
+ * [B, Hkv, S_cap, d] bf16 become codes times scale, rounded to nearest even
+ * (exact for the scales that bd_cache_append_q8 writes); later rows are left
+ * as they are.  A cache_len[i] outside [0, S_cap] leaves that sequence's rows
+ * and records BD_ERR_DEVICE_TIMEOUT in the device status word.
+ * Errors: as bd_cache_append_q8, plus BD_ERR_INVALID_ARG for aliased outputs.
+ */
+BD_API bd_status bd_cache_read_q8(const void *k_cache, const void *v_cache,
+                                  const float *k_scale, const float *v_scale,
+                                  const int32_t *cache_len, void *k_out,
+                                  void *v_out, int B, int Hkv, int d, int S_cap,
+                                  int group, struct CUstream_st *stream);
+
+/*
+ * Block decode over the cache in 8 bits: what bd_attn_decode computes, with
+ * the keys and values codes times scale.  Same masks and modes, same q_blk,
+ * out, lse, cache_len and workspace; the block's own rows are in the cache at
+ * cache_len[i] .. cache_len[i]+b-1 in modes 0 and 1 (bd_cache_append_q8 with
+ * advance = 0).  Codes of positions that no row of the block sees are not
+ * used, NaN codes among them; in mode 1 a NaN value in one of the block's own
+ * V rows reaches every row of the block.  A query row with an infinity or a
+ * NaN gives NaN.
+ *
+ * Errors: as bd_attn_decode and, for the cache, bd_cache_append_q8.
+ */
+BD_API bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache,
+                                   const void *v_cache, const float *k_scale,
+                                   const float *v_scale, const int32_t *cache_len,
+                                   void *out, float *lse, int B, int Hq, int Hkv,
+                                   int b, int d, int intra_block_mode,
+                                   struct CUstream_st *stream, int S_cap,
+                                   int group, void *workspace,
+                                   size_t workspace_bytes);
+
+/*
+ * Verify drafted tokens against the target's probabilities, with the random
+ * numbers given: speculative sampling, where bd_spec_accept compares tokens.
+ *
+ * Position j of sequence i is accepted while u q(x) < p(x): x = draft[i][j],
+ * q and p its probabilities in rows j of draft_prob[i] and target_prob[i], u =
+ * u_accept[i][j]; decided exactly (the product in fp64).  n_accept[i] = n, the
+ * number of positions before the first refusal.  next_token[i] is drawn from
+ * the weights max(p_n - q_n, 0) of row n, or from p_n if they are all 0, or if
+ * every position was accepted (n = n_draft[i]): the lowest t whose running sum
+ * w_0 + .. + w_t exceeds u_sample[i] times the sum of all (sums in fp64; the
+ * last t with a weight if rounding leaves none).  A weight that is NaN counts
+ * as 0; without any mass next_token[i] is -1.
+ *
+ *   draft        [B, b] int32, DEVICE
+ *   draft_prob   [B, b, V] fp32, DEVICE, or NULL: the draft was not sampled,
+ *                q is 1 at the drafted token and 0 elsewhere
+ *   target_prob  [B, b + 1, V] fp32, DEVICE
+ *   u_accept     [B, b] fp32, u_sample [B] fp32, DEVICE, in [0, 1)
+ *   n_draft      [B] int32, DEVICE, drafted positions, or NULL: b each
+ *   n_accept, next_token  [B] int32, DEVICE (written)
+ *
+ * A sequence with n_draft[i] outside [0, b] or a drafted token outside [0, V)
+ * gets n_accept 0 and next_token -1, and the device status word records
+ * BD_ERR_DEVICE_TIMEOUT.  Errors: BD_ERR_INVALID_ARG for a null or misaligned
+ * pointer, a size <= 0 or one buffer for both outputs; BD_ERR_UNSUPPORTED for
+ * V > 4194304; BD_ERR_CUDA if the launch fails.
+ */
+BD_API bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
+                                const float *target_prob, const float *u_accept,
+                                const float *u_sample, const int32_t *n_draft,
+                                int32_t *n_accept, int32_t *next_token, int B,
+                                int b, int V, struct CUstream_st *stream);
+
 /* Bytes of scratch bd_attn_decode needs for these sizes (0 on bad sizes).
  * Pure host arithmetic; needs no GPU. */
 BD_API size_t bd_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int b, int d,
