@@ -768,6 +768,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 constexpr int kCombineRowsPerWarp = 4;
 constexpr int kCombineRowGroups = kTcM / (8 * kCombineRowsPerWarp);
 
+// KEEP_NAN: a row with a NaN in one of its pieces has lse NaN (the cache in 8
+// bits promises it), else -inf.
+template <bool KEEP_NAN>
 __global__ void __launch_bounds__(256)
     bd_decode_stream_combine_kernel(const PParams p)
 {
@@ -845,7 +848,7 @@ __global__ void __launch_bounds__(256)
         if (lane * 4 < p.d)
             reinterpret_cast<uint2 *>(p.out + orow * p.d)[lane] = o2;
         if (lane == 0)
-            p.lse[orow] = z[k] > 0.f ? m[k] + __logf(z[k]) : -INFINITY;
+            p.lse[orow] = z[k] > 0.f ? m[k] + __logf(z[k]) : KEEP_NAN && z[k] != 0.f ? NAN : -INFINITY;
     }
 }
 

@@ -8,7 +8,7 @@
 // which also runs block decode; the backward in attn_tc_bwd.cuh; the cache
 // and SPRINT kernels in cache_ops.cuh.  The serving step over a cache in 8
 // bits: rope.cuh (positions), cache_q8.cuh (writing and reading the cache),
-// attn_q8.cuh (decode), spec_verify.cuh (verification).
+// attn_q8_tc.cuh (decode), spec_verify.cuh (verification).
 #include "bd_attn.h"
 #include "bd_attn_debug.h"
 
@@ -27,7 +27,7 @@
 #include "attn_tc_persist.cuh"
 #include "attn_tc_pair.cuh"
 #include "attn_tc_bwd.cuh"
-#include "attn_q8.cuh"
+#include "attn_q8_tc.cuh"
 #include "bd_common.cuh"
 #include "cache_ops.cuh"
 #include "cache_q8.cuh"
@@ -232,6 +232,23 @@ bool make_map_rows(CUtensorMap *m, const void *base, uint64_t n1, uint64_t n2,
     return r == CUDA_SUCCESS;
 }
 
+// 3-D map over e4m3 codes [n2][n1][d]: boxes of 128 codes x 128 rows x 1,
+// 128-byte swizzle; columns past d and rows past n1 read as zero.
+bool make_map_codes(CUtensorMap *m, const void *base, uint64_t n1, uint64_t n2, uint64_t d)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    cuuint64_t dims[3] = {d, n1, n2};
+    cuuint64_t strides[2] = {d, d * n1};
+    cuuint32_t box[3] = {128, 128, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_map_rows128(CUtensorMap *m, const void *base, uint64_t n1,
                       uint64_t n2, uint64_t d = 128)
 {
@@ -317,6 +334,27 @@ bd_status decode_validate(const void *q_blk, const void *k_cache,
     return BD_OK;
 }
 
+// Programmatic dependent launch of the merge of cut units: its blocks may be
+// placed while the attention kernel before it runs; they wait for its end
+// in-kernel.
+template <bool KEEP_NAN>
+bd_status launch_combine(const bd::PParams &p, int G, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(G, bd::kCombineRowGroups);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, bd::bd_decode_stream_combine_kernel<KEEP_NAN>, p) != cudaSuccess)
+        return BD_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
 // Launches block decode with a validated plan and a workspace of at least
 // pl.total_bytes (256-byte aligned).
 bd_status decode_launch(const void *q_blk, const void *k_cache,
@@ -354,21 +392,7 @@ bd_status decode_launch(const void *q_blk, const void *k_cache,
         bd_status st = launch_persist<1>(mq, mk, mv, p, G, stream);
         if (st != BD_OK)
             return st;
-        // programmatic dependent launch: the combine's blocks may be placed
-        // while the attention kernel runs; they wait for its end in-kernel
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(G, bd::kCombineRowGroups);
-        cfg.blockDim = dim3(256);
-        cfg.dynamicSmemBytes = 0;
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, bd::bd_decode_stream_combine_kernel, p) != cudaSuccess)
-            return BD_ERR_CUDA;
-        return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+        return launch_combine<false>(p, G, stream);
     }
 }
 
@@ -380,6 +404,26 @@ inline bool aligned4(const void *p)
 
 // Group sizes of a cache in 8 bits: whole 16-key chunks of a key tile.
 inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
+
+// The kernel moves registers between its warpgroups: it runs only if the
+// compiled kernel's registers per thread cover the split.
+template <int DH>
+bd_status launch_q8_tc(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
+                       int grid, cudaStream_t st)
+{
+    static std::atomic<int> usable{-1};
+    if (usable.load() < 0) {
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, bd::bd_decode_q8_tc_kernel<DH>) != cudaSuccess)
+            return BD_ERR_CUDA;
+        usable.store(a.numRegs * bd::kQtThreads >=
+                     2 * 128 * bd::kQtRegsSoftmax + 128 * bd::kQtRegsOther);
+    }
+    if (usable.load() != 1 || set_smem<bd::bd_decode_q8_tc_kernel<DH>>(bd::kQtSmemBytes) != BD_OK)
+        return BD_ERR_CUDA;
+    bd::bd_decode_q8_tc_kernel<DH><<<grid, bd::kQtThreads, bd::kQtSmemBytes, st>>>(mk, mv, p);
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
 
 // Host-side checks shared by the calls on a cache in 8 bits.
 bd_status q8_cache_validate(const void *k_cache, const void *v_cache, const float *k_scale,
@@ -893,27 +937,38 @@ bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache, const void *
     if (workspace) {
         if ((reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < pl.total_bytes)
             return BD_ERR_INVALID_ARG;
+    } else {
+        st = get_internal_workspace(pl.total_bytes, &workspace);
+        if (st != BD_OK)
+            return st;
     }
-    bd::Q8Attn p = {};
+    bd::QtParams p = {};
+    p.pp.out = static_cast<bf16 *>(out);
+    p.pp.lse = lse;
+    p.pp.part_o = static_cast<float *>(workspace);
+    p.pp.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.o_bytes);
+    p.pp.cut_desc = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + pl.o_bytes + pl.lse_bytes);
+    p.pp.cache_len = cache_len;
+    p.pp.B = B; p.pp.Hq = Hq; p.pp.Hkv = Hkv; p.pp.b = b; p.pp.d = d;
+    p.pp.nkeys = S_cap;
+    p.pp.mode = intra_block_mode;
+    p.pp.row_tiles = pl.row_tiles;
+    p.pp.rows_unit = (Hq / Hkv) * b;
+    p.pp.scale_log2 = (1.0f / std::sqrt((float)d)) * bd::kLog2e;
     p.q = static_cast<const bf16 *>(q_blk);
-    p.k = static_cast<const uint8_t *>(k_cache);
-    p.v = static_cast<const uint8_t *>(v_cache);
     p.ks = k_scale;
     p.vs = v_scale;
-    p.cache_len = cache_len;
-    p.out = static_cast<bf16 *>(out);
-    p.lse = lse;
-    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.b = b; p.d = d; p.S_cap = S_cap;
-    p.T = group; p.groups = (int)cdiv(S_cap, group); p.mode = intra_block_mode;
-    p.scale_log2 = (1.0f / std::sqrt((float)d)) * bd::kLog2e;
-    const unsigned grid = (unsigned)cdiv((long long)B * Hq * b, 4);
-    if (d == 128)
-        bd::bd_decode_q8_simt_kernel<128><<<grid, 128, 0, stream>>>(p);
-    else if (d == 64)
-        bd::bd_decode_q8_simt_kernel<64><<<grid, 128, 0, stream>>>(p);
-    else
-        bd::bd_decode_q8_simt_kernel<32><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+    p.groups = (int)cdiv(S_cap, group);
+    p.tshift = group == 16 ? 4 : group == 32 ? 5 : group == 64 ? 6 : 7;
+    CUtensorMap mk, mv;
+    if (!make_map_codes(&mk, k_cache, (uint64_t)S_cap, (uint64_t)B * Hkv, d) ||
+        !make_map_codes(&mv, v_cache, (uint64_t)S_cap, (uint64_t)B * Hkv, d))
+        return BD_ERR_CUDA;
+    const int G = persistent_grid();
+    st = d == 128  ? launch_q8_tc<128>(mk, mv, p, G, stream)
+         : d == 64 ? launch_q8_tc<64>(mk, mv, p, G, stream)
+                   : launch_q8_tc<32>(mk, mv, p, G, stream);
+    return st == BD_OK ? launch_combine<true>(p.pp, G, stream) : st;
 }
 
 bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,

@@ -376,9 +376,9 @@ BD_API size_t bd_sprint_workspace_bytes(int B, int S_cap);
  *                     values are its codes times its group's scale
  *   group             16, 32, 64 or 128
  * bd_cache_append_q8 writes powers of two between 2^-64 and 2^120 as scales.
- * The reading calls take any positive finite scale in the groups that hold
- * visible positions; codes and scales behind them are never used, whatever
- * they hold.
+ * The reading calls take any scale from 2^-100 to 2^120 in the groups that
+ * hold visible positions (bd_attn_decode_q8 works with both the scale and its
+ * inverse); codes and scales behind them are never used, whatever they hold.
  */
 
 /* Scalings of bd_rope_table. */
