@@ -16,20 +16,20 @@
 // Persistent, one CTA per SM, over the work list of the bf16 decode
 // (DecSource: whole units, or equal ranges of 128-key tiles merged by
 // bd_decode_stream_combine_kernel).  Roles:
-//   warps 0-3, 4-7  softmax, thread = query row = TMEM lane; the two
-//                   warpgroups take alternate key tiles, so one computes
-//                   exponentials while the other waits for its product
-//   warp 8          TMA of K and V, cp.async of the scales, the work list
-//   warp 9          MMA issue: QK_0, then QK_{j+1}, PV_j for every tile, over
-//                   segment boundaries
-//   warps 10, 11    per tile: the table of scales, V codes to f16
-// TMEM: S/P of even and odd tiles (128 columns each; P, f16, over its own S),
-// O (128), two buffers of Q (hi and lo, 32 columns each).
+//   warps 0-3, 4-7  softmax, thread = query row = TMEM lane; one warpgroup
+//                   takes the first 64 keys of every tile, one the last
+//   warp 8          the work list, TMA of K
+//   warp 9          MMA issue: the QK of a tile, then the PVs of the tile
+//                   before, step by step, over segment boundaries
+//   warp 10         TMA of V, cp.async of the scales
+//   warps 12-15     per tile: the table of scales, V codes to f16
+// TMEM: S/P of two tiles (64 columns a step; P, f16, over its own S), O (128),
+// two buffers of Q (hi and lo, 32 columns each).
 //
-// O has one running maximum.  It is handed from tile to tile, warpgroup to
-// warpgroup, in shared memory, before the exponentials: a tile waits for the
+// O has one running maximum.  It is handed from step to step, warpgroup to
+// warpgroup, in shared memory, before the exponentials: a step waits for the
 // one before it only with its maximum in hand.  Each warpgroup has its own sum
-// l, relative to the maximum at its last tile; the epilogue joins the two.
+// l, relative to the maximum at its last step; the epilogue joins the two.
 #pragma once
 
 #include "attn_tc_persist.cuh"
@@ -37,16 +37,12 @@
 
 namespace bd {
 
-constexpr int kQtThreads = 384;
-constexpr int kQtRegsSoftmax = 208; // setmaxnreg of warpgroups 0 and 1
-constexpr int kQtRegsOther = 88;    // setmaxnreg of warpgroup 2
-static_assert(2 * 128 * kQtRegsSoftmax + 128 * kQtRegsOther <=
-                  kQtThreads * (65536 / kQtThreads / 8 * 8),
-              "register split above the launch's allocation");
+constexpr int kQtThreads = 512;
 
 constexpr int kQtTile = kTcN * kTcD; // bytes of a key tile's codes
 constexpr int kQtKStages = 4, kQtVStages = 4;
 constexpr int kQtChunks = kTcN / 16; // runs of 16 keys: one scale each
+constexpr int kQtStep = 64;          // keys per softmax step: two steps a tile
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
 constexpr int kQtSmemK = 0;
@@ -108,20 +104,26 @@ __device__ __forceinline__ float lg2(float x)
 // smallest normal one then 2^-20 of the row's largest P.
 constexpr float kQtTop = 6.f, kQtLazy = 8.f;
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // A query row as two halves of e4m3 codes in tensor memory, hi in columns
-// [tq, tq + 32), lo behind it, and its scale; thread = row.
+// [tq, tq + 32), lo behind it, and its scale; thread = row.  The row is read
+// twice (the second time from L1), which saves 64 registers.
 template <int DH>
 __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint32_t tq)
 {
-    uint4 w[DH / 8];
-#pragma unroll
-    for (int i = 0; i < DH / 8; ++i)
-        w[i] = valid ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+    const uint4 *row = reinterpret_cast<const uint4 *>(src);
     float amax = 0.f;
     bool finite = true;
 #pragma unroll
     for (int i = 0; i < DH / 8; ++i) {
-        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        const uint4 w = valid ? row[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const float a = fabsf(__uint_as_float(ws[t] << 16));
@@ -133,26 +135,30 @@ __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint3
     // 2^-k q reaches 448 at most; k stays where 2^k and 2^-k are normal
     const int k = max(q8_scale_exp(finite ? amax : 0.f), -100);
     const float inv = finite ? exp2_int(-k) : NAN;
-    uint32_t hi[32], lo[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        hi[i] = lo[i] = 0;
+    for (int c = 0; c < DH / 32; ++c) { // 32 dims
+        uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int i = 0; i < DH / 8; ++i) {
-        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int i = 0; i < 4; ++i) {
+            const uint4 w = valid ? row[4 * c + i] : make_uint4(0, 0, 0, 0);
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+            uint32_t h[4], r[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float a = __uint_as_float(ws[t] << 16) * inv;
-            const float b = __uint_as_float(ws[t] & 0xffff0000u) * inv;
-            const uint16_t h = e4m3x2(a, b);
-            const float2 f = float2_of_e4m3x2(h);
-            const uint16_t r = e4m3x2(a - f.x, b - f.y);
-            hi[2 * i + (t >> 1)] |= (uint32_t)h << (16 * (t & 1));
-            lo[2 * i + (t >> 1)] |= (uint32_t)r << (16 * (t & 1));
+            for (int t = 0; t < 4; ++t) {
+                const float a = __uint_as_float(ws[t] << 16) * inv;
+                const float b = __uint_as_float(ws[t] & 0xffff0000u) * inv;
+                h[t] = e4m3x2(a, b);
+                const float2 f = float2_of_e4m3x2((uint16_t)h[t]);
+                r[t] = e4m3x2(a - f.x, b - f.y);
+            }
+            hi[2 * i] = h[0] | h[1] << 16;
+            hi[2 * i + 1] = h[2] | h[3] << 16;
+            lo[2 * i] = r[0] | r[1] << 16;
+            lo[2 * i + 1] = r[2] | r[3] << 16;
         }
+        tmem_st8(tq + 8 * c, hi);
+        tmem_st8(tq + 32 + 8 * c, lo);
     }
-    tmem_st32(tq, hi);
-    tmem_st32(tq + 32, lo);
     return finite ? exp2_int(k) : NAN;
 }
 
@@ -171,21 +177,22 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     auto bar_kempty = [&](int s) { return bar0 + 32 + 8 * s; };
     auto bar_vfull = [&](int s) { return bar0 + 64 + 8 * s; };
     auto bar_vempty = [&](int s) { return bar0 + 96 + 8 * s; };
-    auto bar_tab = [&](int s) { return bar0 + 128 + 8 * s; };   // table of tile j & 3
-    auto bar_ifull = [&](int s) { return bar0 + 160 + 8 * s; }; // segment si & 3
-    auto bar_iempty = [&](int s) { return bar0 + 192 + 8 * s; };
-    auto bar_w = [&](int s) { return bar0 + 224 + 8 * s; };     // V of tile j & 1 in f16
-    auto bar_sfull = [&](int s) { return bar0 + 240 + 8 * s; };
-    auto bar_pfull = [&](int s) { return bar0 + 256 + 8 * s; };
-    auto bar_odone = [&](int s) { return bar0 + 272 + 8 * s; }; // PV of tile j & 1
-    auto bar_mtok = [&](int s) { return bar0 + 288 + 8 * s; };  // maximum handed on
+    auto bar_ifull = [&](int s) { return bar0 + 128 + 8 * s; }; // segment si & 3
+    auto bar_iempty = [&](int s) { return bar0 + 160 + 8 * s; };
+    auto bar_sfull = [&](int s) { return bar0 + 192 + 8 * s; }; // S of tile j & 1, and its scales
+    auto bar_pfull = [&](int s) { return bar0 + 224 + 8 * s; }; // P of step t & 3
+    auto bar_w = [&](int s) { return bar0 + 256 + 8 * s; };     // V of tile j & 1 in f16
+    auto bar_wfree = [&](int s) { return bar0 + 272 + 8 * s; }; // both its PVs done
     auto bar_qfull = [&](int s) { return bar0 + 304 + 8 * s; };
-    const uint32_t bar_l = bar0 + 320;     // both sums of a segment written
-    const uint32_t bar_ofree = bar0 + 328; // O read out
-    const uint32_t bar_final = bar0 + 336;
+    // maximum of step t & 1 handed on, 32 rows each
+    auto bar_mtok = [&](int s, int w) { return bar0 + 320 + 32 * s + 8 * w; };
+    const uint32_t bar_l = bar0 + 384;     // both sums of a segment written
+    const uint32_t bar_ofree = bar0 + 392; // O read out
+    const uint32_t bar_final = bar0 + 400;
+    auto bar_odone = [&](int s) { return bar0 + 408 + 8 * s; }; // PV of step t & 3
     static_assert(kQtKStages == 4 && kQtVStages == 4, "barrier layout");
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 384);
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 392);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 448);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 456);
     Seg *seg_ring = reinterpret_cast<Seg *>(sbase + kQtSmemSeg); // nt = 0: no more
     float *s_m = reinterpret_cast<float *>(sbase + kQtSmemM);
     float2 *s_l = reinterpret_cast<float2 *>(sbase + kQtSmemL);
@@ -200,18 +207,19 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             mbar_init(bar_kfull(s), 1);
             mbar_init(bar_kempty(s), 1);
             mbar_init(bar_vfull(s), 1 + 2 * kQtChunks); // + a copy of each scale
-            mbar_init(bar_vempty(s), 2);
-            mbar_init(bar_tab(s), 1);
+            mbar_init(bar_vempty(s), 4);
             mbar_init(bar_ifull(s), 1);
-            mbar_init(bar_iempty(s), 11); // 8 softmax warps, MMA, 2 converters
+            mbar_init(bar_iempty(s), 14); // 8 softmax warps, MMA, V, 4 converters
+            mbar_init(bar_pfull(s), 4);
+            mbar_init(bar_odone(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar_w(s), 2);
-            mbar_init(bar_sfull(s), 1);
-            mbar_init(bar_pfull(s), 128);
-            mbar_init(bar_odone(s), 1);
-            mbar_init(bar_mtok(s), 128);
+            mbar_init(bar_sfull(s), 2); // the MMA, the table
+            mbar_init(bar_w(s), 4);
+            mbar_init(bar_wfree(s), 1);
             mbar_init(bar_qfull(s), 128);
+            for (int w = 0; w < 4; ++w)
+                mbar_init(bar_mtok(s, w), 1);
         }
         mbar_init(bar_l, 256);
         mbar_init(bar_ofree, 256);
@@ -237,10 +245,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     // a barrier wait by a converged warp
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort_flag); };
 
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQtRegsOther));
     if (warp == 8) {
-        // -------------------------- work list; loads of K, V and the scales
+        // ------------------------------------------ work list, loads of K
         DecSource src;
         src.init(p.pp);
         if (lane == 0)
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         Seg sg;
         bool ok = true;
         int g = 0; // running tile counter
-        int kiss = 0, viss = 0;
+        int kiss = 0;
         for (int si = 0; ok; ++si) {
             const int slot = si & 3;
             if (si >= 4 && !(ok = wait(bar_iempty(slot), (uint32_t)(((si - 4) >> 2) & 1))))
@@ -270,36 +276,62 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             if (!got)
                 break;
             for (int it = 0; it < sg.nt; ++it, ++g) {
-                const int ks = sg.lo0 + it * kTcN;
                 const int s = g & 3;
-                const uint32_t par = (uint32_t)((g >> 2) & 1) ^ 1u;
-                if (g >= 4 && !(ok = wait(bar_kempty(s), par)))
+                if (g >= 4 && !(ok = wait(bar_kempty(s), (uint32_t)((g >> 2) & 1) ^ 1u)))
                     break;
                 // injected fault: this tile never arrives
                 const bool skip = g == 0 && blockIdx.x == 0 && lane == 0 &&
                                   atomicExch(&g_fault_skip_k, 0) != 0;
                 if (lane == 0 && !skip) {
                     mbar_expect_tx(bar_kfull(s), kQtTile);
-                    tma_load_3d(base + kQtSmemK + s * kQtTile, &tm_k, 0, ks, sg.kvhead, bar_kfull(s));
+                    tma_load_3d(base + kQtSmemK + s * kQtTile, &tm_k, 0, sg.lo0 + it * kTcN, sg.kvhead,
+                                bar_kfull(s));
                     kiss = g + 1;
                 }
-                if (g >= 4 && !(ok = wait(bar_vempty(s), par)))
+                __syncwarp();
+            }
+        }
+        // wait (bounded) for every copy this role issued
+        if (lane == 0) {
+            const long long c0 = clock64();
+            for (int x = kiss > 4 ? kiss - 4 : 0; x < kiss; ++x)
+                while (!mbar_try_wait(bar_kfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
+                       clock64() - c0 < kWaitCycles) {}
+        }
+    } else if (warp == 10) {
+        // ------------------------------------- loads of V and the scales
+        bool ok = true;
+        int g = 0, viss = 0;
+        for (int si = 0; ok; ++si) {
+            if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
+                break;
+            const Seg &sg = seg_ring[si & 3];
+            const int nt = sg.nt, lo = sg.lo0, hi = sg.hi0, head = sg.kvhead;
+            __syncwarp();
+            if (nt == 0)
+                break;
+            if (lane == 0)
+                mbar_arrive(bar_iempty(si & 3));
+            for (int it = 0; it < nt; ++it, ++g) {
+                const int ks = lo + it * kTcN;
+                const int s = g & 3;
+                if (g >= 4 && !(ok = wait(bar_vempty(s), (uint32_t)((g >> 2) & 1) ^ 1u)))
                     break;
                 if (lane == 0) {
                     mbar_expect_tx(bar_vfull(s), kQtTile);
-                    tma_load_3d(base + kQtSmemV + s * kQtTile, &tm_v, 0, ks, sg.kvhead, bar_vfull(s));
+                    tma_load_3d(base + kQtSmemV + s * kQtTile, &tm_v, 0, ks, head, bar_vfull(s));
                     viss = g + 1;
                 }
                 // lanes 0-7: scales of K, 8-15: of V; chunks with no visible
                 // key read nothing
                 if (lane < 2 * kQtChunks) {
                     const int key = ks + 16 * (lane & 7);
-                    const bool in = key < sg.hi0;
-                    const float *src_s = (lane < 8 ? p.ks : p.vs) + (size_t)sg.kvhead * p.groups +
-                                         (in ? key >> p.tshift : 0);
+                    const bool in = key < hi;
+                    const float *src = (lane < 8 ? p.ks : p.vs) + (size_t)head * p.groups +
+                                       (in ? key >> p.tshift : 0);
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
                                      base + kQtSmemRaw + s * 64 + lane * 4),
-                                 "l"(src_s), "r"(in ? 4 : 0)
+                                 "l"(src), "r"(in ? 4 : 0)
                                  : "memory");
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                                      bar_vfull(s))
@@ -308,13 +340,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 __syncwarp();
             }
         }
-        // wait (bounded) for every copy this role issued
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0) {
             const long long c0 = clock64();
-            for (int x = kiss > 4 ? kiss - 4 : 0; x < kiss; ++x)
-                while (!mbar_try_wait(bar_kfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
-                       clock64() - c0 < kWaitCycles) {}
             for (int x = viss > 4 ? viss - 4 : 0; x < viss; ++x)
                 while (!mbar_try_wait(bar_vfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
                        clock64() - c0 < kWaitCycles) {}
@@ -326,80 +354,102 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         // O has DH columns; a 64-column half of V at least
         constexpr uint32_t idesc_pv = idesc_fmt0(kTcM, DH > 64 ? 128 : 64, 1);
         bool ok = true;
-        // cursor of the QKs: tile qj of the CTA, the qi-th of segment qs
-        int qj = 0, qi = 0, qs = 0, qnt = 0;
-        auto next_qk = [&]() -> bool { // false: no more tiles, or aborted
-            if (qi == qnt) {
-                if (qnt) { // segment qs is through
+        // cursor of the QKs: tile qj of the CTA, tile qi of the qn of its segment qs
+        int qj = 0, qi = 0, qn = 0, qs = 0;
+        // cursor of the PVs: tile j of the CTA, tile i of the n of its segment si
+        int j = 0, i = 0, n = 0, si = 0;
+        int hi = 0; // keys of the segment from its first tile on
+        auto next_qk = [&]() { // the next tile's QK, if there is one to issue
+            if (qi == qn) {
+                // One segment ahead of the PVs at most: the queries behind
+                // that are split only after PVs that wait in this loop.
+                if (qn && qs > si)
+                    return;
+                if (qn) { // segment qs is through
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(bar_iempty(qs & 3));
                     ++qs;
+                    qn = qi = 0;
                 }
                 if (!(ok = wait(bar_ifull(qs & 3), (uint32_t)((qs >> 2) & 1))))
-                    return false;
-                qnt = seg_ring[qs & 3].nt;
-                qi = 0;
-                if (qnt == 0)
-                    return false;
-                if (!(ok = wait(bar_qfull(qs & 1), (uint32_t)((qs >> 1) & 1))))
-                    return false;
+                    return;
+                qn = seg_ring[qs & 3].nt;
+                if (qn == 0 || !(ok = wait(bar_qfull(qs & 1), (uint32_t)((qs >> 1) & 1))))
+                    return;
             }
             const int s = qj & 3;
             if (!(ok = wait(bar_kfull(s), (uint32_t)((qj >> 2) & 1))))
-                return false;
+                return;
             tc_fence_after();
-            // the S buffer held P of tile qj - 2, whose PV was issued before
-            const uint32_t ts = tmem + (uint32_t)(qj & 1) * 128;
+            // the S buffer held P of tile qj - 2, whose PVs were issued before
+            const uint32_t ts = tmem + (uint32_t)(qj & 1) * kTcN;
             const uint32_t tq = t_q + (uint32_t)(qs & 1) * 64;
             const uint32_t kb = base + kQtSmemK + (uint32_t)s * kQtTile;
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int kk = 0; kk < DH / 32; ++kk)
-                    tc_mma8_ts_p(ts, tq + half * 32 + kk * 8, smem_desc_sw128(kb + kk * 32, 16, 1024),
-                                 idesc_qk, half || kk ? 1u : 0u, ld);
+                    tc_mma8_ts_p(ts, tq + h * 32 + kk * 8, smem_desc_sw128(kb + kk * 32, 16, 1024),
+                                 idesc_qk, h || kk ? 1u : 0u, ld);
             tc_commit_p(bar_sfull(qj & 1), ld);
             tc_commit_p(bar_kempty(s), ld);
             ++qj;
             ++qi;
-            return true;
         };
-        int j = 0, si = 0; // PV: tile of the CTA, segment
-        bool first = true; // first tile of its segment
-        bool more = next_qk();
-        while (ok && more) {
-            // tile j is the last of its segment if the next QK opens another
-            const bool last = qi == qnt;
-            more = next_qk();
-            if (!ok)
-                break;
+        next_qk();
+        while (ok && j < qj) {
+            if (i == n) {
+                // known: QK_j was issued, and a slot of the ring is not
+                // rewritten before this segment's epilogue
+                n = seg_ring[si & 3].nt;
+                hi = seg_ring[si & 3].hi0 - seg_ring[si & 3].lo0;
+                i = 0;
+            }
+            if (qj == j + 1) { // QK_{j+1} goes out before the PVs of tile j
+                next_qk();
+                if (!ok)
+                    break;
+            }
             // O was last read out by the epilogue of segment si - 1
-            if (first && si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1))))
+            if (i == 0 && si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1))))
                 break;
             const int b = j & 1;
-            if (!(ok = wait(bar_w(b), (uint32_t)((j >> 1) & 1))) ||
-                !(ok = wait(bar_pfull(b), (uint32_t)((j >> 1) & 1))))
+            if (!(ok = wait(bar_w(b), (uint32_t)((j >> 1) & 1))))
                 break;
-            tc_fence_after();
-            const uint32_t vb = base + kQtSmemW + (uint32_t)b * kTileBytes;
-            const uint32_t tp = tmem + (uint32_t)b * 128;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int pb = 2 * b + half;
+                if (!(ok = wait(bar_pfull(pb), (uint32_t)((j >> 1) & 1))))
+                    break;
+                tc_fence_after();
+                const uint32_t vb = base + kQtSmemW + (uint32_t)b * kTileBytes + half * (kQtStep * 128);
+                const uint32_t tp = tmem + (uint32_t)pb * kQtStep;
+                if (half == 0 || i * kTcN + kQtStep < hi) {
 #pragma unroll
-            for (int kk = 0; kk < kTcN / 16; ++kk)
-                tc_mma_ts_p(t_o, tp + kk * 8, smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024),
-                            idesc_pv, (!first || kk > 0) ? 1u : 0u, ld);
-            tc_commit_p(bar_odone(b), ld);
-            first = last;
-            si += last ? 1 : 0;
+                    for (int kk = 0; kk < kQtStep / 16; ++kk)
+                        tc_mma_ts_p(t_o, tp + kk * 8,
+                                    smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024), idesc_pv,
+                                    (i > 0 || half > 0 || kk > 0) ? 1u : 0u, ld);
+                }
+                tc_commit_p(bar_odone(pb), ld);
+            }
+            if (!ok)
+                break;
+            tc_commit_p(bar_wfree(b), ld);
             ++j;
+            if (++i == n)
+                ++si;
+            if (qj == j)
+                next_qk();
         }
         tc_commit_p(bar_final, ld);
         const long long c0 = clock64();
         while (!mbar_try_wait(bar_final, 0) && clock64() - c0 < kWaitCycles) {}
         __syncwarp();
-    } else {
+    } else if (warp >= 12) {
         // ------------------------- the table of scales, V codes to f16
-        const int cw = warp - 10;
+        const int cw = warp - 12;
         bool ok = true;
         int j = 0;
         for (int si = 0; ok; ++si) {
@@ -413,55 +463,59 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 const int s = j & 3, ks = lo + it * kTcN;
                 if (!(ok = wait(bar_vfull(s), (uint32_t)((j >> 2) & 1))))
                     break;
-                // the table slot was last read for tile j - 4, whose P the PV
-                // that tile j - 1's conversion waited for had used
+                // the f16 buffer was last read by the PVs of tile j - 2;
+                // the softmax of that tile lies behind them
+                const int b = j & 1;
+                if (j >= 2 && !(ok = wait(bar_wfree(b), (uint32_t)(((j - 2) >> 1) & 1))))
+                    break;
                 if (cw == 0) {
                     if (lane < kQtChunks) {
-                        float4 t = make_float4(1.f, 0.f, 0.f, 0.f);
+                        float4 e = make_float4(1.f, 0.f, 0.f, 0.f);
                         if (ks + 16 * lane < hi) {
                             const float sv = s_raw[s * 16 + 8 + lane];
-                            t.x = s_raw[s * 16 + lane] * p.pp.scale_log2;
-                            t.y = lg2(sv);
-                            t.z = 1.f / sv;
+                            e.x = s_raw[s * 16 + lane] * p.pp.scale_log2;
+                            e.y = lg2(sv);
+                            e.z = 1.f / sv;
                         }
-                        s_tab[(j & 3) * kQtChunks + lane] = t;
+                        s_tab[(j & 3) * kQtChunks + lane] = e;
                     }
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(bar_tab(j & 3));
+                        mbar_arrive(bar_sfull(b));
                 }
-                // the f16 buffer was last read by PV_{j-2}
-                const int b = j & 1;
-                if (j >= 2 && !(ok = wait(bar_odone(b), (uint32_t)(((j - 2) >> 1) & 1))))
-                    break;
                 // 8 lanes take half a row each of rows r and r ^ 5 (64 codes
                 // = 4 vectors of 16): their reads of the swizzled codes and
                 // their writes of the swizzled halves each cover all banks.
                 const uint32_t src = base + kQtSmemV + (uint32_t)s * kQtTile;
                 const uint32_t dst = base + kQtSmemW + (uint32_t)b * kTileBytes;
-                const int hrow = (lane >> 3) * 2;                  // 0, 2, 4, 6
+                // rows of 8: pairs (0, 5), (2, 7), (4, 1), (6, 3)
+                const int hrow = (lane >> 3) * 2;
+                const int r8 = (lane & 4) ? (hrow ^ 5) : hrow;
                 const int u4 = lane & 3;
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    // warp cw: half (i & 1) of rows 64 cw + 8 (i >> 1) ..
-                    const int half = i & 1;
-                    if (half && DH <= 64)
-                        continue;
-                    // rows of 8: pairs (0, 5), (2, 7), (4, 1), (6, 3)
-                    const int r8 = (lane & 4) ? (hrow ^ 5) : hrow;
-                    const int r = 64 * cw + 8 * (i >> 1) + r8;
-                    uint32_t x[4];
+                constexpr int H = DH <= 64 ? 1 : 2; // halves of 64 columns
+                // warp cw: rows 32 cw .. 32 cw + 31; all loads go out first
+                uint32_t x[4 * H][4];
+#pragma unroll
+                for (int i = 0; i < 4 * H; ++i) {
+                    const int r = 32 * cw + 8 * (i / H) + r8;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                 : "r"(src + r * 128 + (((half * 4 + u4) ^ r8) << 4))
+                                 : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
+                                 : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
                                  : "memory");
-                    if (ks + r >= hi) // not a key: no code of it may be used
-                        x[0] = x[1] = x[2] = x[3] = 0;
+                }
+                if (ks + 32 * cw + 32 > hi) { // not keys: no code of theirs may be used
+#pragma unroll
+                    for (int i = 0; i < 4 * H; ++i)
+                        if (ks + 32 * cw + 8 * (i / H) + r8 >= hi)
+                            x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < 4 * H; ++i) {
                     uint32_t y[8];
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
-                        y[t] = half2_of_e4m3x2((uint16_t)(x[t >> 1] >> (16 * (t & 1))));
-                    const uint32_t row = dst + half * kHalfTileBytes + r * 128;
+                        y[t] = half2_of_e4m3x2((uint16_t)(x[i][t >> 1] >> (16 * (t & 1))));
+                    const uint32_t row = dst + (i % H) * kHalfTileBytes + (32 * cw + 8 * (i / H) + r8) * 128;
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
                                      row + (((2 * u4) ^ r8) << 4)),
                                  "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
@@ -482,10 +536,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             if (ok && lane == 0)
                 mbar_arrive(bar_iempty(si & 3));
         }
-    }
-    } else {
+    } else if (warp < 8) {
         // ------------------------------------------- softmax and epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQtRegsSoftmax));
         const int wg = warp >> 2;
         const int row = threadIdx.x & (kTcM - 1);
         const int wrow = row & ~31; // first row of this warp
@@ -507,129 +559,136 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             mbar_arrive(bar_qfull(si & 1));
             return true;
         };
-        bool ok = wg == 0 || split(0);
-        int j = 0; // running tile counter at the segment's start
+        bool ok = wg == 1 || split(0);
+        int j0 = 0; // tile of the CTA at the segment's start
         for (int si = 0; ok; ++si) {
             if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
                 break;
             const Seg &sg = seg_ring[si & 3];
-            const int nt = sg.nt;
-            if (nt == 0)
+            if (sg.nt == 0)
                 break;
             if (!(ok = wait(bar_qfull(si & 1), (uint32_t)((si >> 1) & 1))))
                 break;
             const float qs = s_qs[(si & 1) * kTcM + row];
-            const int nrows = sg.nrows, lo = sg.lo0;
+            const int n = sg.nt, nrows = sg.nrows, lo = sg.lo0;
             const int full_end = min(sg.fhi0, sg.hi0); // keys that every row sees
             const int jr = (sg.qrow0 + min(row, nrows - 1)) % p.pp.b;
             // keys that this row sees
             const int seen = min(sg.hi0, sg.len + (p.pp.mode == 0 ? p.pp.b : p.pp.mode == 1 ? jr + 1 : 0));
             const bool live = wrow < nrows; // a warp without rows only arrives
             float m_own = -INFINITY, l = 0.f;
-            for (int jj = (j & 1) == wg ? 0 : 1; jj < nt; jj += 2) {
-                const int jg = j + jj, b = jg & 1;
-                const uint32_t ts = tmem + (uint32_t)b * 128 + lane_off;
-                if (!(ok = wait(bar_sfull(b), (uint32_t)((jg >> 1) & 1))))
+            for (int i = 0; i < n; ++i) {
+                const int j = j0 + i, t = 2 * j + wg; // tile, step
+                const uint32_t ts = tmem + (uint32_t)(t & 3) * kQtStep + lane_off;
+                const int ks = lo + i * kTcN + wg * kQtStep;
+                if (!(ok = wait(bar_sfull(j & 1), (uint32_t)((j >> 1) & 1))))
                     break;
-                if (!live) {
-                    mbar_arrive(bar_mtok(b));
-                    mbar_arrive(bar_pfull(b));
+                if (!live || ks >= sg.hi0) { // no rows, or (in the last step) no keys
+                    if (t >= 1 && !(ok = wait(bar_mtok(wg ^ 1, warp & 3), (uint32_t)(((t - 1) >> 1) & 1))))
+                        break;
+                    s_m[wg * kTcM + row] = s_m[(wg ^ 1) * kTcM + row];
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar_mtok(wg, warp & 3));
+                        mbar_arrive(bar_pfull(t & 3));
+                    }
                     continue;
                 }
-                if (!(ok = wait(bar_tab(jg & 3), (uint32_t)((jg >> 2) & 1))))
-                    break;
                 tc_fence_after();
-                uint32_t sr[kTcN];
-                tmem_ld32x4_wait(ts, ts + 32, ts + 64, ts + 96, sr, sr + 32, sr + 64, sr + 96);
-                float s[kTcN];
+                uint32_t sr[kQtStep];
+                tmem_ld32x2_wait(ts, ts + 32, sr, sr + 32);
+                float s[kQtStep];
 #pragma unroll
-                for (int c = 0; c < kTcN; ++c)
+                for (int c = 0; c < kQtStep; ++c)
                     s[c] = __uint_as_float(sr[c]);
-                const int ks = lo + jj * kTcN;
-                if (ks + kTcN > full_end) {
+                if (ks + kQtStep > full_end) {
 #pragma unroll
-                    for (int w = 0; w < kTcN / 32; ++w) {
+                    for (int w = 0; w < kQtStep / 32; ++w) {
                         const uint32_t mk = range_bits(0, seen - ks - 32 * w);
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             s[32 * w + c] = ((mk >> c) & 1u) ? s[32 * w + c] : -INFINITY;
                     }
                 }
-                const float4 *tab = s_tab + (jg & 3) * kQtChunks;
+                constexpr int C = kQtStep / 16;
+                const float4 *tab = s_tab + (j & 3) * kQtChunks + wg * C;
+                float4 e[C];
                 float mt = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < kQtChunks; ++c) {
+                for (int c = 0; c < C; ++c) {
                     const float *x = s + 16 * c;
                     const float m0 = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
                     const float m1 = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
-                    const float4 t = tab[c];
+                    e[c] = tab[c];
                     // the product is no less than 2^-126: a masked score has
                     // to stay -inf (and below that x is 0 anyway)
-                    mt = fmaxf(mt, fmaf(fmaxf(m0, m1), fmaxf(t.x * qs, 1.2e-38f), t.y));
+                    e[c].x = fmaxf(e[c].x * qs, 1.2e-38f);
+                    mt = fmaxf(mt, fmaf(fmaxf(m0, m1), e[c].x, e[c].y));
                 }
-                // the maximum up to the tile before
-                if (jg >= 1 && !(ok = wait(bar_mtok(b ^ 1), (uint32_t)(((jg - 1) >> 1) & 1))))
+                // the maximum up to the step before
+                if (t >= 1 && !(ok = wait(bar_mtok(wg ^ 1, warp & 3), (uint32_t)(((t - 1) >> 1) & 1))))
                     break;
-                const float m_prev = jj == 0 ? -INFINITY : s_m[(b ^ 1) * kTcM + row];
+                const bool first = i == 0 && wg == 0; // of the segment
+                const float m_prev = first ? -INFINITY : s_m[(wg ^ 1) * kTcM + row];
                 const bool need = mt > m_prev + (kQtTop + kQtLazy);
                 const float m = need ? mt - kQtTop : m_prev;
                 // the TMEM read-modify-write of O is warp-collective
-                if (jj > 0 && __any_sync(0xffffffffu, need)) {
-                    if (!(ok = wait(bar_odone(b ^ 1), (uint32_t)(((jg - 1) >> 1) & 1))))
+                if (!first && __any_sync(0xffffffffu, need)) {
+                    // PV_{t-1}.  Its barrier's phase before, PV_{t-5}, is of
+                    // tile j - 2 or older, whose PVs QK_j was issued behind.
+                    if (!(ok = wait(bar_odone((t - 1) & 3), (uint32_t)(((t - 1) >> 2) & 1))))
                         break;
                     tc_fence_after();
                     const float c = !need ? 1.f : m_prev == -INFINITY ? 0.f : ex2(m_prev - m);
-#pragma unroll
+#pragma unroll 1
                     for (int q4 = 0; q4 < DH / 32; ++q4) {
                         uint32_t o[32];
                         tmem_ld32_wait(t_o + lane_off + q4 * 32, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+                        for (int x = 0; x < 32; ++x)
+                            o[x] = __float_as_uint(__uint_as_float(o[x]) * c);
                         tmem_st32(t_o + lane_off + q4 * 32, o);
                     }
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                s_m[b * kTcM + row] = m;
-                mbar_arrive(bar_mtok(b));
+                s_m[wg * kTcM + row] = m;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_mtok(wg, warp & 3));
                 if (m > m_own) {
                     l = m_own == -INFINITY ? l : l * ex2(m_own - m); // 0, or NaN for good
                     m_own = m;
                 }
                 const float nm = m == -INFINITY ? 0.f : -m;
+                uint32_t pk[kQtStep / 2];
 #pragma unroll
-                for (int c2 = 0; c2 < kQtChunks / 2; ++c2) {
-                    uint32_t pk[16];
+                for (int c = 0; c < C; ++c) {
+                    const float o = e[c].y + nm;
+                    float r0 = 0.f, r1 = 0.f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float4 t = tab[2 * c2 + h];
-                        const float a = fmaxf(t.x * qs, 1.2e-38f);
-                        const float o = t.y + nm;
-                        float r0 = 0.f, r1 = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const int x = (2 * c2 + h) * 16 + i;
-                            float y0, y1;
-                            ffma2(y0, y1, s[x], s[x + 1], a, a, o, o);
-                            y0 = ex2(y0);
-                            y1 = ex2(y1);
-                            fadd2(r0, r1, r0, r1, y0, y1);
-                            pk[h * 8 + i / 2] = pack_f16x2(y0, y1);
-                        }
-                        l = fmaf(r0 + r1, t.z, l);
+                    for (int x = 16 * c; x < 16 * c + 16; x += 2) {
+                        float y0, y1;
+                        ffma2(y0, y1, s[x], s[x + 1], e[c].x, e[c].x, o, o);
+                        y0 = ex2(y0);
+                        y1 = ex2(y1);
+                        fadd2(r0, r1, r0, r1, y0, y1);
+                        pk[x / 2] = pack_f16x2(y0, y1);
                     }
-                    tmem_st16(ts + c2 * 16, pk);
+                    l = fmaf(r0 + r1, e[c].z, l);
                 }
+                tmem_st32(ts, pk);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar_pfull(b));
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_pfull(t & 3));
             }
             if (!ok)
                 break;
-            const int jl = j + nt - 1; // last tile of the segment
-            // the warpgroup without the last tile readies the next queries
-            if ((jl & 1) != wg && !(ok = split(si + 1)))
+            const int jl = j0 + n - 1; // last tile of the segment
+            // the warpgroup without the last step readies the next queries
+            if (wg == 0 && !(ok = split(si + 1)))
                 break;
             s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float2(l, m_own);
             mbar_arrive(bar_l);
@@ -640,9 +699,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const float l0 = m_own == -INFINITY ? l : l * ex2(m_own - m);
             const float l1 = other.y == -INFINITY ? other.x : other.x * ex2(other.y - m);
             l = l0 + l1; // a NaN shows in l whatever m is
-            // both warpgroups are past their tiles, so QK_jl has finished,
-            // and with it PV_{jl-2}: the wait for PV_jl cannot mistake it
-            if (!(ok = wait(bar_odone(jl & 1), (uint32_t)((jl >> 1) & 1))))
+            // the last PV; the PVs of tile jl - 2 lie behind QK_jl, which both
+            // warpgroups have seen
+            if (!(ok = wait(bar_odone(2 * (jl & 1) + 1), (uint32_t)((jl >> 1) & 1))))
                 break;
             tc_fence_after();
             const bool valid = row < nrows;
@@ -687,7 +746,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_iempty(si & 3));
-            j += nt;
+            j0 += n;
         }
     }
 

@@ -405,21 +405,11 @@ inline bool aligned4(const void *p)
 // Group sizes of a cache in 8 bits: whole 16-key chunks of a key tile.
 inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
 
-// The kernel moves registers between its warpgroups: it runs only if the
-// compiled kernel's registers per thread cover the split.
 template <int DH>
 bd_status launch_q8_tc(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
                        int grid, cudaStream_t st)
 {
-    static std::atomic<int> usable{-1};
-    if (usable.load() < 0) {
-        cudaFuncAttributes a;
-        if (cudaFuncGetAttributes(&a, bd::bd_decode_q8_tc_kernel<DH>) != cudaSuccess)
-            return BD_ERR_CUDA;
-        usable.store(a.numRegs * bd::kQtThreads >=
-                     2 * 128 * bd::kQtRegsSoftmax + 128 * bd::kQtRegsOther);
-    }
-    if (usable.load() != 1 || set_smem<bd::bd_decode_q8_tc_kernel<DH>>(bd::kQtSmemBytes) != BD_OK)
+    if (set_smem<bd::bd_decode_q8_tc_kernel<DH>>(bd::kQtSmemBytes) != BD_OK)
         return BD_ERR_CUDA;
     bd::bd_decode_q8_tc_kernel<DH><<<grid, bd::kQtThreads, bd::kQtSmemBytes, st>>>(mk, mv, p);
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
