@@ -13,23 +13,25 @@
 // memory, at the price of one bf16 product.  V's codes become f16 (exact) on
 // their way to the second product, since P needs more than e4m3's 4 bits.
 //
-// Persistent, one CTA per SM, over the work list of the bf16 decode
-// (DecSource: whole units, or equal ranges of 128-key tiles merged by
-// bd_decode_stream_combine_kernel).  Roles:
+// Persistent, one CTA per SM, over units of a sequence, a kv-head and 128
+// query rows: whole ones, or equal ranges of 128-key tiles whose pieces
+// bd_decode_stream_combine_kernel merges (QtSource).  Roles:
 //   warps 0-3, 4-7  softmax, thread = query row = TMEM lane; one warpgroup
 //                   takes the first 64 keys of every tile, one the last
 //   warp 8          the work list, TMA of K
 //   warp 9          MMA issue: the QK of a tile, then the PVs of the tile
-//                   before, step by step, over segment boundaries
+//                   before, over segment boundaries
 //   warp 10         TMA of V, cp.async of the scales
-//   warps 12-15     per tile: the table of scales, V codes to f16
-// TMEM: S/P of two tiles (64 columns a step; P, f16, over its own S), O (128),
-// two buffers of Q (hi and lo, 32 columns each).
+//   warps 12-15     V codes to f16; the table of scales; at the end of a
+//                   segment the next one's queries
+// TMEM: S of one tile (128 columns), P of the two halves (f16, 32 each), an O
+// for each warpgroup (128 each), Q (hi and lo, 32 each).
 //
-// O has one running maximum.  It is handed from step to step, warpgroup to
-// warpgroup, in shared memory, before the exponentials: a step waits for the
-// one before it only with its maximum in hand.  Each warpgroup has its own sum
-// l, relative to the maximum at its last step; the epilogue joins the two.
+// A warpgroup reads its half of S into registers at once, so the next tile's
+// QK runs under its exponentials, and keeps an O, a running maximum and a sum
+// of its own: the two meet only in the epilogue, which joins them.  (With one
+// O and the maximum handed from step to step a step took 2500 cycles, a third
+// of them for the hand-over and the wait for S.)
 #pragma once
 
 #include "attn_tc_persist.cuh"
@@ -50,13 +52,117 @@ constexpr int kQtSmemV = kQtSmemK + kQtKStages * kQtTile;
 constexpr int kQtSmemW = kQtSmemV + kQtVStages * kQtTile; // V in f16: 2 buffers
 constexpr int kQtSmemRaw = kQtSmemW + 2 * kTileBytes;     // scales, 16 a stage
 constexpr int kQtSmemTab = kQtSmemRaw + kQtVStages * 64;  // 4 tables of 8 float4
-constexpr int kQtSmemM = kQtSmemTab + 4 * kQtChunks * 16; // running maxima [2][128]
-constexpr int kQtSmemL = kQtSmemM + 2 * kTcM * 4;         // (l, M) [2][2][128]
+constexpr int kQtSmemL = kQtSmemTab + 4 * kQtChunks * 16; // (l, M) [2][2][128]
 constexpr int kQtSmemQs = kQtSmemL + 4 * kTcM * 8;        // row scales of Q [2][128]
 constexpr int kQtSmemSeg = kQtSmemQs + 2 * kTcM * 4;      // 4 segments, 128 B each
 constexpr int kQtSmemBar = kQtSmemSeg + 4 * 128;
 constexpr int kQtSmemBytes = kQtSmemBar + 512 + 1024; // + alignment slack
 static_assert(kQtSmemBytes <= 227 * 1024, "more shared memory than a CTA may have");
+
+// The work list, walked by one converged warp.  It is DecSource's (units x
+// tiles, cut into equal ranges, or whole units) but for three things: the
+// warp reads 32 lengths at a time (one after another they took 3 us for 16
+// sequences and 8 us for 64, at the head of every launch); no more CTAs take
+// part than there are tiles, so that the merge of a short launch walks over no
+// empty pieces; and units stay whole only where the longest is at most 3 tiles
+// above the mean of the CTAs, about what merging costs.
+struct QtSource {
+    long long t, t1, t0, T;
+    long long seq_base;
+    int seq, seq_tiles, len, G;
+
+    __device__ static int tiles_of(const PParams &p, int i, int &len)
+    {
+        len = i < p.B ? p.cache_len[i] : 0;
+        return i < p.B ? max(0, decode_unit_tiles(len, p.b, p.nkeys, p.mode)) : 0;
+    }
+    __device__ void init(const PParams &p)
+    {
+        const int lane = threadIdx.x & 31;
+        const int ups = p.Hkv * p.row_tiles; // units per sequence
+        long long sum = 0;
+        int maxt = 0, n;
+        for (int i = lane; i < p.B; i += 32) {
+            const int ti = tiles_of(p, i, n);
+            sum += ti;
+            maxt = max(maxt, ti);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        maxt = __reduce_max_sync(0xffffffffu, maxt);
+        T = sum * ups;
+        G = (int)min((long long)gridDim.x, max(T, 1LL));
+        const long long units = (long long)p.B * ups;
+        t = t0 = t1 = seq_base = 0;
+        seq = seq_tiles = len = 0;
+        if (units <= gridDim.x && (long long)(maxt - 3) * G <= T) {
+            // CTA c takes unit c
+            if (blockIdx.x < units) {
+                seq = blockIdx.x / ups;
+                seq_tiles = tiles_of(p, seq, len);
+                t = t0 = (long long)(blockIdx.x % ups) * seq_tiles;
+                t1 = t0 + seq_tiles;
+            }
+            return;
+        }
+        if ((int)blockIdx.x >= G)
+            return;
+        t = t0 = range_start(T, G, blockIdx.x);
+        t1 = range_start(T, G, blockIdx.x + 1);
+        // the sequence that holds tile t0 < T
+        for (int i0 = 0; i0 < p.B; i0 += 32) {
+            const long long mine = (long long)tiles_of(p, i0 + lane, n) * ups;
+            long long incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += up;
+            }
+            const int before = __popc(__ballot_sync(0xffffffffu, seq_base + incl <= t0));
+            if (before < 32) {
+                seq_base += __shfl_sync(0xffffffffu, incl - mine, before);
+                seq = i0 + before;
+                break;
+            }
+            seq_base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        seq_tiles = tiles_of(p, seq, len);
+    }
+    __device__ bool next(const PParams &p, Seg &sg)
+    {
+        if (t >= t1)
+            return false;
+        const int ups = p.Hkv * p.row_tiles;
+        while (t >= seq_base + (long long)ups * seq_tiles) {
+            seq_base += (long long)ups * seq_tiles;
+            seq_tiles = tiles_of(p, ++seq, len);
+        }
+        const long long local = t - seq_base;
+        const int uis = (int)(local / seq_tiles); // unit inside the sequence
+        const int kt0 = (int)(local % seq_tiles);
+        const int n = (int)min((long long)(seq_tiles - kt0), t1 - t);
+        const int g = uis / p.row_tiles, rt = uis % p.row_tiles;
+        sg.kvhead = seq * p.Hkv + g;
+        sg.qrow0 = rt * kTcM;
+        sg.nrows = min(kTcM, p.rows_unit - rt * kTcM);
+        sg.lo0 = kt0 * kTcN;
+        sg.hi0 = min((kt0 + n) * kTcN, len + decode_own_keys(p.b, p.mode));
+        sg.fhi0 = len + (p.mode == 0 ? p.b : 0);
+        sg.nt = n;
+        sg.len = len;
+        sg.out_row0 = (seq * p.Hq + g * (p.Hq / p.Hkv)) * p.b + rt * kTcM;
+        sg.complete = n == seq_tiles;
+        const long long u0 = seq_base + (long long)uis * seq_tiles;
+        sg.slot = u0 < t0 ? 0 : 1;
+        // range x starts at floor(T x / G), so the last x starting at or
+        // before tile e is floor(((e + 1) G - 1) / T)
+        sg.last_cta = !sg.complete && sg.slot == 1 ? (int)(((u0 + seq_tiles) * G - 1) / T) : -1;
+        t += n;
+        return true;
+    }
+};
 
 struct QtParams {
     PParams pp; // sizes, outputs and scratch, as the bf16 decode's
@@ -111,19 +217,20 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
                  : "memory");
 }
 
-// A query row as two halves of e4m3 codes in tensor memory, hi in columns
-// [tq, tq + 32), lo behind it, and its scale; thread = row.  The row is read
-// twice (the second time from L1), which saves 64 registers.
+// A query row as two halves of e4m3 codes, and its scale.
 template <int DH>
-__device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint32_t tq)
+__device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint32_t *hi, uint32_t *lo)
 {
     const uint4 *row = reinterpret_cast<const uint4 *>(src);
+    uint4 w[DH / 8];
+#pragma unroll
+    for (int i = 0; i < DH / 8; ++i)
+        w[i] = valid ? row[i] : make_uint4(0, 0, 0, 0);
     float amax = 0.f;
     bool finite = true;
 #pragma unroll
     for (int i = 0; i < DH / 8; ++i) {
-        const uint4 w = valid ? row[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const float a = fabsf(__uint_as_float(ws[t] << 16));
@@ -136,28 +243,21 @@ __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint3
     const int k = max(q8_scale_exp(finite ? amax : 0.f), -100);
     const float inv = finite ? exp2_int(-k) : NAN;
 #pragma unroll
-    for (int c = 0; c < DH / 32; ++c) { // 32 dims
-        uint32_t hi[8], lo[8];
+    for (int i = 0; i < DH / 8; ++i) {
+        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t h[4], r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 w = valid ? row[4 * c + i] : make_uint4(0, 0, 0, 0);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-            uint32_t h[4], r[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float a = __uint_as_float(ws[t] << 16) * inv;
-                const float b = __uint_as_float(ws[t] & 0xffff0000u) * inv;
-                h[t] = e4m3x2(a, b);
-                const float2 f = float2_of_e4m3x2((uint16_t)h[t]);
-                r[t] = e4m3x2(a - f.x, b - f.y);
-            }
-            hi[2 * i] = h[0] | h[1] << 16;
-            hi[2 * i + 1] = h[2] | h[3] << 16;
-            lo[2 * i] = r[0] | r[1] << 16;
-            lo[2 * i + 1] = r[2] | r[3] << 16;
+        for (int t = 0; t < 4; ++t) {
+            const float a = __uint_as_float(ws[t] << 16) * inv;
+            const float b = __uint_as_float(ws[t] & 0xffff0000u) * inv;
+            h[t] = e4m3x2(a, b);
+            const float2 f = float2_of_e4m3x2((uint16_t)h[t]);
+            r[t] = e4m3x2(a - f.x, b - f.y);
         }
-        tmem_st8(tq + 8 * c, hi);
-        tmem_st8(tq + 32 + 8 * c, lo);
+        hi[2 * i] = h[0] | h[1] << 16;
+        hi[2 * i + 1] = h[2] | h[3] << 16;
+        lo[2 * i] = r[0] | r[1] << 16;
+        lo[2 * i + 1] = r[2] | r[3] << 16;
     }
     return finite ? exp2_int(k) : NAN;
 }
@@ -179,22 +279,23 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     auto bar_vempty = [&](int s) { return bar0 + 96 + 8 * s; };
     auto bar_ifull = [&](int s) { return bar0 + 128 + 8 * s; }; // segment si & 3
     auto bar_iempty = [&](int s) { return bar0 + 160 + 8 * s; };
-    auto bar_sfull = [&](int s) { return bar0 + 192 + 8 * s; }; // S of tile j & 1, and its scales
-    auto bar_pfull = [&](int s) { return bar0 + 224 + 8 * s; }; // P of step t & 3
+    const uint32_t bar_sread = bar0 + 192; // S read by both warpgroups
+    const uint32_t bar_qfull = bar0 + 200;
+    const uint32_t bar_qfree = bar0 + 208; // last QK of a segment done
+    auto bar_pfull = [&](int w) { return bar0 + 224 + 8 * w; }; // P of warpgroup w
+    auto bar_odone = [&](int w) { return bar0 + 240 + 8 * w; }; // its PV done
     auto bar_w = [&](int s) { return bar0 + 256 + 8 * s; };     // V of tile j & 1 in f16
     auto bar_wfree = [&](int s) { return bar0 + 272 + 8 * s; }; // both its PVs done
-    auto bar_qfull = [&](int s) { return bar0 + 304 + 8 * s; };
-    // maximum of step t & 1 handed on, 32 rows each
-    auto bar_mtok = [&](int s, int w) { return bar0 + 320 + 32 * s + 8 * w; };
-    const uint32_t bar_l = bar0 + 384;     // both sums of a segment written
-    const uint32_t bar_ofree = bar0 + 392; // O read out
-    const uint32_t bar_final = bar0 + 400;
-    auto bar_odone = [&](int s) { return bar0 + 408 + 8 * s; }; // PV of step t & 3
+    // S of tile j & 1, its scales and those of the queries: one buffer of S,
+    // but the converters arrive up to a tile ahead
+    auto bar_sfull = [&](int s) { return bar0 + 312 + 8 * s; };
+    const uint32_t bar_l = bar0 + 288;     // both sums of a segment written
+    const uint32_t bar_ofree = bar0 + 296; // both O read out
+    const uint32_t bar_final = bar0 + 304;
     static_assert(kQtKStages == 4 && kQtVStages == 4, "barrier layout");
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 448);
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 456);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 336);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 344);
     Seg *seg_ring = reinterpret_cast<Seg *>(sbase + kQtSmemSeg); // nt = 0: no more
-    float *s_m = reinterpret_cast<float *>(sbase + kQtSmemM);
     float2 *s_l = reinterpret_cast<float2 *>(sbase + kQtSmemL);
     float *s_qs = reinterpret_cast<float *>(sbase + kQtSmemQs);
     float4 *s_tab = reinterpret_cast<float4 *>(sbase + kQtSmemTab);
@@ -210,19 +311,19 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             mbar_init(bar_vempty(s), 4);
             mbar_init(bar_ifull(s), 1);
             mbar_init(bar_iempty(s), 14); // 8 softmax warps, MMA, V, 4 converters
-            mbar_init(bar_pfull(s), 4);
-            mbar_init(bar_odone(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar_sfull(s), 2); // the MMA, the table
+            mbar_init(bar_pfull(s), 4);
+            mbar_init(bar_odone(s), 1);
             mbar_init(bar_w(s), 4);
             mbar_init(bar_wfree(s), 1);
-            mbar_init(bar_qfull(s), 128);
-            for (int w = 0; w < 4; ++w)
-                mbar_init(bar_mtok(s, w), 1);
+            mbar_init(bar_sfull(s), 5); // the MMA, 4 converters
         }
+        mbar_init(bar_sread, 8);
+        mbar_init(bar_qfull, 4);
+        mbar_init(bar_qfree, 1);
         mbar_init(bar_l, 256);
-        mbar_init(bar_ofree, 256);
+        mbar_init(bar_ofree, 8);
         mbar_init(bar_final, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -237,7 +338,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t t_o = tmem + 256, t_q = tmem + 384;
+    const uint32_t t_p = tmem + 128, t_o = tmem + 192, t_q = tmem + 448;
     // the combine kernel may be scheduled now; it reads nothing of this
     // launch before the whole grid has finished
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -247,7 +348,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 
     if (warp == 8) {
         // ------------------------------------------ work list, loads of K
-        DecSource src;
+        QtSource src;
         src.init(p.pp);
         if (lane == 0)
             p.pp.cut_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -356,101 +457,109 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         bool ok = true;
         // cursor of the QKs: tile qj of the CTA, tile qi of the qn of its segment qs
         int qj = 0, qi = 0, qn = 0, qs = 0;
-        // cursor of the PVs: tile j of the CTA, tile i of the n of its segment si
-        int j = 0, i = 0, n = 0, si = 0;
-        int hi = 0; // keys of the segment from its first tile on
-        auto next_qk = [&]() { // the next tile's QK, if there is one to issue
+        auto next_qk = [&]() { // the next tile's QK, if there is one
             if (qi == qn) {
-                // One segment ahead of the PVs at most: the queries behind
-                // that are split only after PVs that wait in this loop.
-                if (qn && qs > si)
-                    return;
-                if (qn) { // segment qs is through
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar_iempty(qs & 3));
-                    ++qs;
-                    qn = qi = 0;
-                }
                 if (!(ok = wait(bar_ifull(qs & 3), (uint32_t)((qs >> 2) & 1))))
                     return;
                 qn = seg_ring[qs & 3].nt;
-                if (qn == 0 || !(ok = wait(bar_qfull(qs & 1), (uint32_t)((qs >> 1) & 1))))
+                qi = 0;
+                if (qn == 0 || !(ok = wait(bar_qfull, (uint32_t)(qs & 1))))
                     return;
+                ++qs;
             }
             const int s = qj & 3;
-            if (!(ok = wait(bar_kfull(s), (uint32_t)((qj >> 2) & 1))))
+            if (!(ok = wait(bar_kfull(s), (uint32_t)((qj >> 2) & 1))) ||
+                (qj >= 1 && !(ok = wait(bar_sread, (uint32_t)((qj - 1) & 1)))))
                 return;
             tc_fence_after();
-            // the S buffer held P of tile qj - 2, whose PVs were issued before
-            const uint32_t ts = tmem + (uint32_t)(qj & 1) * kTcN;
-            const uint32_t tq = t_q + (uint32_t)(qs & 1) * 64;
             const uint32_t kb = base + kQtSmemK + (uint32_t)s * kQtTile;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int kk = 0; kk < DH / 32; ++kk)
-                    tc_mma8_ts_p(ts, tq + h * 32 + kk * 8, smem_desc_sw128(kb + kk * 32, 16, 1024),
+                    tc_mma8_ts_p(tmem, t_q + h * 32 + kk * 8, smem_desc_sw128(kb + kk * 32, 16, 1024),
                                  idesc_qk, h || kk ? 1u : 0u, ld);
             tc_commit_p(bar_sfull(qj & 1), ld);
             tc_commit_p(bar_kempty(s), ld);
             ++qj;
-            ++qi;
+            if (++qi == qn)
+                tc_commit_p(bar_qfree, ld);
         };
         next_qk();
-        while (ok && j < qj) {
-            if (i == n) {
-                // known: QK_j was issued, and a slot of the ring is not
-                // rewritten before this segment's epilogue
-                n = seg_ring[si & 3].nt;
-                hi = seg_ring[si & 3].hi0 - seg_ring[si & 3].lo0;
-                i = 0;
-            }
-            if (qj == j + 1) { // QK_{j+1} goes out before the PVs of tile j
+        int j = 0; // tile of the PVs
+        for (int si = 0; ok && j < qj; ++si) {
+            // known, as its first QK was issued
+            const int n = seg_ring[si & 3].nt, hi = seg_ring[si & 3].hi0 - seg_ring[si & 3].lo0;
+            for (int i = 0; i < n; ++i, ++j) {
                 next_qk();
+                const int b = j & 1;
+                // O was last read out by the epilogue of segment si - 1
+                if (!ok || (i == 0 && si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1)))) ||
+                    !(ok = wait(bar_w(b), (uint32_t)((j >> 1) & 1))))
+                    break;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = wait(bar_pfull(half), (uint32_t)(j & 1))))
+                        break;
+                    tc_fence_after();
+                    const uint32_t vb = base + kQtSmemW + (uint32_t)b * kTileBytes + half * (kQtStep * 128);
+                    // (the last tile may have no key in its second half)
+                    if (half == 0 || i * kTcN + kQtStep < hi) {
+#pragma unroll
+                        for (int kk = 0; kk < kQtStep / 16; ++kk)
+                            tc_mma_ts_p(t_o + half * 128, t_p + half * 32 + kk * 8,
+                                        smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024),
+                                        idesc_pv, (i > 0 || kk > 0) ? 1u : 0u, ld);
+                    }
+                    tc_commit_p(bar_odone(half), ld);
+                }
                 if (!ok)
                     break;
+                tc_commit_p(bar_wfree(b), ld);
             }
-            // O was last read out by the epilogue of segment si - 1
-            if (i == 0 && si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1))))
-                break;
-            const int b = j & 1;
-            if (!(ok = wait(bar_w(b), (uint32_t)((j >> 1) & 1))))
-                break;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const int pb = 2 * b + half;
-                if (!(ok = wait(bar_pfull(pb), (uint32_t)((j >> 1) & 1))))
-                    break;
-                tc_fence_after();
-                const uint32_t vb = base + kQtSmemW + (uint32_t)b * kTileBytes + half * (kQtStep * 128);
-                const uint32_t tp = tmem + (uint32_t)pb * kQtStep;
-                if (half == 0 || i * kTcN + kQtStep < hi) {
-#pragma unroll
-                    for (int kk = 0; kk < kQtStep / 16; ++kk)
-                        tc_mma_ts_p(t_o, tp + kk * 8,
-                                    smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024), idesc_pv,
-                                    (i > 0 || half > 0 || kk > 0) ? 1u : 0u, ld);
-                }
-                tc_commit_p(bar_odone(pb), ld);
-            }
-            if (!ok)
-                break;
-            tc_commit_p(bar_wfree(b), ld);
-            ++j;
-            if (++i == n)
-                ++si;
-            if (qj == j)
-                next_qk();
+            __syncwarp();
+            if (ok && lane == 0)
+                mbar_arrive(bar_iempty(si & 3));
         }
         tc_commit_p(bar_final, ld);
         const long long c0 = clock64();
         while (!mbar_try_wait(bar_final, 0) && clock64() - c0 < kWaitCycles) {}
         __syncwarp();
     } else if (warp >= 12) {
-        // ------------------------- the table of scales, V codes to f16
+        // ------- V codes to f16, the table of scales, the split of queries
         const int cw = warp - 12;
-        bool ok = true;
+        const int row = 32 * cw + lane;
+        // The queries of segment si; the buffer was last read by the QKs of
+        // the segment before.
+        auto split = [&](int si) -> bool {
+            if (!wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1)))
+                return false;
+            const Seg &sg = seg_ring[si & 3];
+            if (sg.nt == 0)
+                return true;
+            uint32_t hi[DH / 4], lo[DH / 4];
+            const float qs =
+                qt_split_row<DH>(p.q + ((size_t)sg.out_row0 + row) * DH, row < sg.nrows, hi, lo);
+            // behind the last QK of segment si - 1, which was issued behind
+            // the reads of every earlier segment's S and row scales
+            if (si >= 1 && !wait(bar_qfree, (uint32_t)((si - 1) & 1)))
+                return false;
+            s_qs[(si & 1) * kTcM + row] = qs;
+            tc_fence_after();
+            const uint32_t tq = t_q + ((uint32_t)(32 * cw) << 16);
+#pragma unroll
+            for (int c = 0; c < DH / 32; ++c) {
+                tmem_st8(tq + 8 * c, hi + 8 * c);
+                tmem_st8(tq + 32 + 8 * c, lo + 8 * c);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_qfull);
+            return true;
+        };
+        bool ok = split(0);
         int j = 0;
         for (int si = 0; ok; ++si) {
             if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
@@ -479,10 +588,10 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         }
                         s_tab[(j & 3) * kQtChunks + lane] = e;
                     }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar_sfull(b));
                 }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_sfull(b));
                 // 8 lanes take half a row each of rows r and r ^ 5 (64 codes
                 // = 4 vectors of 16): their reads of the swizzled codes and
                 // their writes of the swizzled halves each cover all banks.
@@ -535,6 +644,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             __syncwarp();
             if (ok && lane == 0)
                 mbar_arrive(bar_iempty(si & 3));
+            ok = ok && split(si + 1);
         }
     } else if (warp < 8) {
         // ------------------------------------------- softmax and epilogue
@@ -542,24 +652,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         const int row = threadIdx.x & (kTcM - 1);
         const int wrow = row & ~31; // first row of this warp
         const uint32_t lane_off = (uint32_t)wrow << 16;
-        // Splits the query rows of segment si, by one warpgroup.  Its buffer
-        // was last read by the QKs of segment si - 2, finished before that
-        // segment's epilogue was.
-        auto split = [&](int si) -> bool {
-            if (!wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1)))
-                return false;
-            const Seg &sg = seg_ring[si & 3];
-            if (sg.nt == 0)
-                return true;
-            const float qs = qt_split_row<DH>(p.q + ((size_t)sg.out_row0 + row) * DH, row < sg.nrows,
-                                              t_q + (uint32_t)(si & 1) * 64 + lane_off);
-            s_qs[(si & 1) * kTcM + row] = qs;
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar_qfull(si & 1));
-            return true;
-        };
-        bool ok = wg == 1 || split(0);
+        const uint32_t ts = tmem + wg * kQtStep + lane_off; // its half of S
+        const uint32_t t_ow = t_o + wg * 128 + lane_off; // this warpgroup's O
+        bool ok = true;
         int j0 = 0; // tile of the CTA at the segment's start
         for (int si = 0; ok; ++si) {
             if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
@@ -567,36 +662,37 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const Seg &sg = seg_ring[si & 3];
             if (sg.nt == 0)
                 break;
-            if (!(ok = wait(bar_qfull(si & 1), (uint32_t)((si >> 1) & 1))))
-                break;
-            const float qs = s_qs[(si & 1) * kTcM + row];
-            const int n = sg.nt, nrows = sg.nrows, lo = sg.lo0;
-            const int full_end = min(sg.fhi0, sg.hi0); // keys that every row sees
+            const int n = sg.nt, nrows = sg.nrows, lo = sg.lo0, hi = sg.hi0;
+            const int full_end = min(sg.fhi0, hi); // keys that every row sees
             const int jr = (sg.qrow0 + min(row, nrows - 1)) % p.pp.b;
             // keys that this row sees
-            const int seen = min(sg.hi0, sg.len + (p.pp.mode == 0 ? p.pp.b : p.pp.mode == 1 ? jr + 1 : 0));
+            const int seen = min(hi, sg.len + (p.pp.mode == 0 ? p.pp.b : p.pp.mode == 1 ? jr + 1 : 0));
             const bool live = wrow < nrows; // a warp without rows only arrives
-            float m_own = -INFINITY, l = 0.f;
+            float qs = 1.f;
+            float m = -INFINITY, l = 0.f; // running maximum (raised lazily), sum
             for (int i = 0; i < n; ++i) {
-                const int j = j0 + i, t = 2 * j + wg; // tile, step
-                const uint32_t ts = tmem + (uint32_t)(t & 3) * kQtStep + lane_off;
+                const int j = j0 + i; // tile
                 const int ks = lo + i * kTcN + wg * kQtStep;
                 if (!(ok = wait(bar_sfull(j & 1), (uint32_t)((j >> 1) & 1))))
                     break;
-                if (!live || ks >= sg.hi0) { // no rows, or (in the last step) no keys
-                    if (t >= 1 && !(ok = wait(bar_mtok(wg ^ 1, warp & 3), (uint32_t)(((t - 1) >> 1) & 1))))
+                if (!live || ks >= hi) { // no rows, or (in the last tile) no keys
+                    if (lane == 0)
+                        mbar_arrive(bar_sread);
+                    if (j >= 1 && !(ok = wait(bar_odone(wg), (uint32_t)((j - 1) & 1))))
                         break;
-                    s_m[wg * kTcM + row] = s_m[(wg ^ 1) * kTcM + row];
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar_mtok(wg, warp & 3));
-                        mbar_arrive(bar_pfull(t & 3));
-                    }
+                    if (lane == 0)
+                        mbar_arrive(bar_pfull(wg));
                     continue;
                 }
+                if (i == 0)
+                    qs = s_qs[(si & 1) * kTcM + row];
                 tc_fence_after();
                 uint32_t sr[kQtStep];
                 tmem_ld32x2_wait(ts, ts + 32, sr, sr + 32);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_sread);
                 float s[kQtStep];
 #pragma unroll
                 for (int c = 0; c < kQtStep; ++c)
@@ -625,40 +721,28 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     e[c].x = fmaxf(e[c].x * qs, 1.2e-38f);
                     mt = fmaxf(mt, fmaf(fmaxf(m0, m1), e[c].x, e[c].y));
                 }
-                // the maximum up to the step before
-                if (t >= 1 && !(ok = wait(bar_mtok(wg ^ 1, warp & 3), (uint32_t)(((t - 1) >> 1) & 1))))
-                    break;
-                const bool first = i == 0 && wg == 0; // of the segment
-                const float m_prev = first ? -INFINITY : s_m[(wg ^ 1) * kTcM + row];
-                const bool need = mt > m_prev + (kQtTop + kQtLazy);
-                const float m = need ? mt - kQtTop : m_prev;
-                // the TMEM read-modify-write of O is warp-collective
-                if (!first && __any_sync(0xffffffffu, need)) {
-                    // PV_{t-1}.  Its barrier's phase before, PV_{t-5}, is of
-                    // tile j - 2 or older, whose PVs QK_j was issued behind.
-                    if (!(ok = wait(bar_odone((t - 1) & 3), (uint32_t)(((t - 1) >> 2) & 1))))
-                        break;
-                    tc_fence_after();
-                    const float c = !need ? 1.f : m_prev == -INFINITY ? 0.f : ex2(m_prev - m);
-#pragma unroll 1
-                    for (int q4 = 0; q4 < DH / 32; ++q4) {
-                        uint32_t o[32];
-                        tmem_ld32_wait(t_o + lane_off + q4 * 32, o);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            o[x] = __float_as_uint(__uint_as_float(o[x]) * c);
-                        tmem_st32(t_o + lane_off + q4 * 32, o);
+                const bool need = mt > m + (kQtTop + kQtLazy);
+                if (__any_sync(0xffffffffu, need)) {
+                    float c = 1.f;
+                    if (need) {
+                        c = m == -INFINITY ? 0.f : ex2(m - (mt - kQtTop));
+                        l = m == -INFINITY ? l : l * c; // 0, or NaN for good
+                        m = mt - kQtTop;
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                }
-                s_m[wg * kTcM + row] = m;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_mtok(wg, warp & 3));
-                if (m > m_own) {
-                    l = m_own == -INFINITY ? l : l * ex2(m_own - m); // 0, or NaN for good
-                    m_own = m;
+                    if (i > 0) { // the TMEM read-modify-write of O is warp-collective
+                        if (!(ok = wait(bar_odone(wg), (uint32_t)((j - 1) & 1))))
+                            break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q4 = 0; q4 < DH / 32; ++q4) {
+                            uint32_t o[32];
+                            tmem_ld32_wait(t_ow + q4 * 32, o);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                o[x] = __float_as_uint(__uint_as_float(o[x]) * c);
+                            tmem_st32(t_ow + q4 * 32, o);
+                        }
+                    }
                 }
                 const float nm = m == -INFINITY ? 0.f : -m;
                 uint32_t pk[kQtStep / 2];
@@ -677,35 +761,39 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     }
                     l = fmaf(r0 + r1, e[c].z, l);
                 }
-                tmem_st32(ts, pk);
+                // P of the tile before has been used
+                if (j >= 1 && !(ok = wait(bar_odone(wg), (uint32_t)((j - 1) & 1))))
+                    break;
+                tc_fence_after();
+                tmem_st32(t_p + wg * 32 + lane_off, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar_pfull(t & 3));
+                    mbar_arrive(bar_pfull(wg));
             }
             if (!ok)
                 break;
             const int jl = j0 + n - 1; // last tile of the segment
-            // the warpgroup without the last step readies the next queries
-            if (wg == 0 && !(ok = split(si + 1)))
-                break;
-            s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float2(l, m_own);
+            s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float2(l, m);
             mbar_arrive(bar_l);
-            if (!(ok = wait(bar_l, (uint32_t)(si & 1))))
-                break;
-            const float2 other = s_l[((si & 1) * 2 + (wg ^ 1)) * kTcM + row];
-            const float m = fmaxf(m_own, other.y);
-            const float l0 = m_own == -INFINITY ? l : l * ex2(m_own - m);
-            const float l1 = other.y == -INFINITY ? other.x : other.x * ex2(other.y - m);
-            l = l0 + l1; // a NaN shows in l whatever m is
-            // the last PV; the PVs of tile jl - 2 lie behind QK_jl, which both
-            // warpgroups have seen
-            if (!(ok = wait(bar_odone(2 * (jl & 1) + 1), (uint32_t)((jl >> 1) & 1))))
+            // both warpgroups' last PVs
+            if (!(ok = wait(bar_l, (uint32_t)(si & 1))) ||
+                !(ok = wait(bar_odone(0), (uint32_t)(jl & 1))) ||
+                !(ok = wait(bar_odone(1), (uint32_t)(jl & 1))))
                 break;
             tc_fence_after();
+            // factors of the two O to the common maximum; O_1 is unwritten
+            // where the segment has no key in a second half
+            const float2 l0 = s_l[(si & 1) * 2 * kTcM + row], l1 = s_l[((si & 1) * 2 + 1) * kTcM + row];
+            const bool two = hi - lo > kQtStep;
+            const float mx = fmaxf(l0.y, l1.y);
+            const float f0 = l0.y == -INFINITY ? 1.f : ex2(l0.y - mx);
+            const float f1 = l1.y == -INFINITY ? 1.f : ex2(l1.y - mx);
+            const float ls = l0.x * f0 + l1.x * f1; // a NaN shows in l whatever m is
+            const float inv = ls == 0.f ? 0.f : 1.f / ls;
+            const float w0 = f0 * inv, w1 = f1 * inv;
             const bool valid = row < nrows;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t grow = (size_t)sg.out_row0 + row;
             const size_t prow = ((size_t)blockIdx.x * 2 + sg.slot) * kTcM + row;
             constexpr int kCols = DH >= 64 ? DH / 2 : DH; // columns of O a warpgroup takes
@@ -713,39 +801,43 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 #pragma unroll
                 for (int q4 = 0; q4 < kCols / 32; ++q4) {
                     const int col = wg * kCols + q4 * 32;
-                    uint32_t o[32];
-                    tmem_ld32_wait(t_o + lane_off + col, o);
+                    uint32_t o[32], o1[32];
+                    tmem_ld32x2_wait(t_o + lane_off + col, t_o + 128 + lane_off + col, o, o1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float x = __uint_as_float(o[i]) * w0;
+                        o[i] = __float_as_uint(two ? fmaf(__uint_as_float(o1[i]), w1, x) : x);
+                    }
                     if (valid && sg.complete) {
                         uint4 *dst = reinterpret_cast<uint4 *>(p.pp.out + grow * DH + col);
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
                             uint4 v4;
-                            v4.x = pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-                            v4.y = pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                            v4.z = pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-                            v4.w = pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                            v4.x = pack_bf16x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1]));
+                            v4.y = pack_bf16x2(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+                            v4.z = pack_bf16x2(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5]));
+                            v4.w = pack_bf16x2(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
                             dst[i / 8] = v4;
                         }
                     } else if (valid) {
-                        float4 *dst = reinterpret_cast<float4 *>(p.pp.part_o + prow * kTcD + col);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.pp.part_o + prow * kTcD + col);
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            dst[i / 4] = make_float4(
-                                __uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                            dst[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
             }
             if (valid && wg == 0)
                 (sg.complete ? p.pp.lse + grow : p.pp.part_lse + prow)[0] =
-                    l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+                    ls == 0.f ? -INFINITY : ((l0.y == -INFINITY && l1.y == -INFINITY ? 0.f : mx) + __log2f(ls)) * kLn2;
             if (!sg.complete && sg.last_cta >= 0 && threadIdx.x == 0)
                 p.pp.cut_desc[blockIdx.x] = make_int4(nrows, sg.last_cta, sg.out_row0, 0);
             tc_fence_before();
-            mbar_arrive(bar_ofree);
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
+                mbar_arrive(bar_ofree);
                 mbar_arrive(bar_iempty(si & 3));
+            }
             j0 += n;
         }
     }
