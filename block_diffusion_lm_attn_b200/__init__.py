@@ -466,31 +466,29 @@ def sprint_prune(k_cache, v_cache, cache_len, conf, modality, alpha=0.5,
 # the serving step over a KV cache in 8 bits
 
 
-def _check_on(t, dtype, shape, device, what):
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()
-            and t.device == device):
+def _check_on(t, dtype, shape, dev, what):
+    """t is a contiguous tensor of this type and shape on CUDA device `dev`
+    (its index).  Written for the good case: a serving step makes five such
+    calls a layer, each with up to eight tensors."""
+    if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and dev >= 0 and t.is_contiguous()):
+        return
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor on %s" %
-                         (what, dtype, device))
-    if t.shape != shape:
-        raise ValueError("%s must have the shape %s" % (what, tuple(shape)))
+                         (what, dtype, "cuda" if dev < 0 else "cuda:%d" % dev))
+    raise ValueError("%s must have the shape %s" % (what, tuple(shape)))
 
 
-class _on:
-    """Makes `device` current for a call if it is not (a launch goes to the
-    current device)."""
-
-    def __init__(self, device):
-        import torch
-        self.guard = (None if device.index == torch.cuda.current_device()
-                      else torch.cuda.device(device))
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(fn, dev, stream, args, tail=()):
+    """fn(*args, stream, *tail) with device `dev` current (a launch goes to the
+    current device); stream None: that device's current stream."""
+    import torch
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, args, tail)
+    handle = (torch._C._cuda_getCurrentRawStream(dev) if stream is None
+              else stream.cuda_stream)
+    return fn(*args, handle, *tail)
 
 
 def rope_table(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
@@ -528,7 +526,7 @@ def rope(q, k, inv_freq, start=None, positions=None, period: int | None = None,
     inputs.  q_out may be q and k_out may be k.  Returns (q_out, k_out)."""
     import torch
     B, Hq, N, d = q.shape
-    dev = q.device
+    dev = q.get_device()
     bf = torch.bfloat16
     _check_on(q, bf, q.shape, dev, "q")
     Hkv = 0
@@ -550,14 +548,13 @@ def rope(q, k, inv_freq, start=None, positions=None, period: int | None = None,
         _check_on(start, torch.int32, (B,), dev, "start")
     if positions is not None:
         _check_on(positions, torch.int32, (B, N), dev, "positions")
-    with _on(dev):
-        st = load().bd_rope(
-            q.data_ptr(), None if k is None else k.data_ptr(),
-            q_out.data_ptr(), None if k is None else k_out.data_ptr(),
-            inv_freq.data_ptr(), None if start is None else start.data_ptr(),
-            None if positions is None else positions.data_ptr(), B, Hq, Hkv, N,
-            d, 2 * inv_freq.numel(), N if period is None else period,
-            int(interleaved), mscale, int(adjoint), _stream_handle(stream))
+    st = _launch(load().bd_rope, dev, stream, (
+        q.data_ptr(), None if k is None else k.data_ptr(),
+        q_out.data_ptr(), None if k is None else k_out.data_ptr(),
+        inv_freq.data_ptr(), None if start is None else start.data_ptr(),
+        None if positions is None else positions.data_ptr(), B, Hq, Hkv, N,
+        d, 2 * inv_freq.numel(), N if period is None else period,
+        int(interleaved), mscale, int(adjoint)))
     if st != BD_OK:
         raise BdAttnError(st, "bd_rope")
     return q_out, k_out
@@ -566,7 +563,7 @@ def rope(q, k, inv_freq, start=None, positions=None, period: int | None = None,
 def _check_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group):
     import torch
     B, Hkv, S_cap, d = shape = k_cache.shape
-    dev = k_cache.device
+    dev = k_cache.get_device()
     if group not in (16, 32, 64, 128):
         raise ValueError("group must be 16, 32, 64 or 128")
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
@@ -605,12 +602,11 @@ def cache_append_q8(k_cache, v_cache, k_scale, v_scale, cache_len, k_new,
         kp, vp = k_new.data_ptr(), v_new.data_ptr()
     if n_new is not None:
         _check_on(n_new, torch.int32, (B,), dev, "n_new")
-    with _on(dev):
-        st = load().bd_cache_append_q8(
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), cache_len.data_ptr(), kp, vp,
-            None if n_new is None else n_new.data_ptr(), B, Hkv, b, d, S_cap,
-            group, int(advance), _stream_handle(stream))
+    st = _launch(load().bd_cache_append_q8, dev, stream, (
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), cache_len.data_ptr(), kp, vp,
+        None if n_new is None else n_new.data_ptr(), B, Hkv, b, d, S_cap,
+        group, int(advance)))
     if st != BD_OK:
         raise BdAttnError(st, "bd_cache_append_q8")
 
@@ -626,16 +622,15 @@ def cache_read_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group: int,
     outs = []
     for t, w in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
-            t = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+            t = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
         else:
             _check_on(t, torch.bfloat16, shape, dev, w)
         outs.append(t)
     k_out, v_out = outs
-    with _on(dev):
-        st = load().bd_cache_read_q8(
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), cache_len.data_ptr(), k_out.data_ptr(),
-            v_out.data_ptr(), B, Hkv, d, S_cap, group, _stream_handle(stream))
+    st = _launch(load().bd_cache_read_q8, dev, stream, (
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), cache_len.data_ptr(), k_out.data_ptr(),
+        v_out.data_ptr(), B, Hkv, d, S_cap, group))
     if st != BD_OK:
         raise BdAttnError(st, "bd_cache_read_q8")
     return k_out, v_out
@@ -657,20 +652,19 @@ def decode_q8(q_blk, k_cache, v_cache, k_scale, v_scale, cache_len, mode: int,
     else:
         _check_on(out, torch.bfloat16, q_blk.shape, dev, "out")
     if lse is None:
-        lse = torch.empty((B, Hq, b), device=dev, dtype=torch.float32)
+        lse = torch.empty((B, Hq, b), device=q_blk.device, dtype=torch.float32)
     else:
         _check_on(lse, torch.float32, (B, Hq, b), dev, "lse")
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous on %s" % dev)
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on cuda:%d" % dev)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    with _on(dev):
-        st = load().bd_attn_decode_q8(
-            q_blk.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), cache_len.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, b, d, mode,
-            _stream_handle(stream), S_cap, group, ws_ptr, ws_bytes)
+    st = _launch(load().bd_attn_decode_q8, dev, stream, (
+        q_blk.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), cache_len.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, b, d, mode),
+        (S_cap, group, ws_ptr, ws_bytes))
     if st != BD_OK:
         raise BdAttnError(st, "bd_attn_decode_q8")
     return out, lse
@@ -686,7 +680,7 @@ def spec_verify(draft, draft_prob, target_prob, u_accept, u_sample,
     import torch
     B, b = draft.shape
     V = target_prob.shape[-1]
-    dev = draft.device
+    dev = draft.get_device()
     i32, f32 = torch.int32, torch.float32
     _check_on(draft, i32, (B, b), dev, "draft")
     _check_on(target_prob, f32, (B, b + 1, V), dev, "target_prob")
@@ -697,20 +691,18 @@ def spec_verify(draft, draft_prob, target_prob, u_accept, u_sample,
     if n_draft is not None:
         _check_on(n_draft, i32, (B,), dev, "n_draft")
     if n_accept is None:
-        n_accept = torch.empty(B, dtype=i32, device=dev)
+        n_accept = torch.empty(B, dtype=i32, device=draft.device)
     else:
         _check_on(n_accept, i32, (B,), dev, "n_accept")
     if next_token is None:
-        next_token = torch.empty(B, dtype=i32, device=dev)
+        next_token = torch.empty(B, dtype=i32, device=draft.device)
     else:
         _check_on(next_token, i32, (B,), dev, "next_token")
-    with _on(dev):
-        st = load().bd_spec_verify(
-            draft.data_ptr(), None if draft_prob is None else draft_prob.data_ptr(),
-            target_prob.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
-            None if n_draft is None else n_draft.data_ptr(),
-            n_accept.data_ptr(), next_token.data_ptr(), B, b, V,
-            _stream_handle(stream))
+    st = _launch(load().bd_spec_verify, dev, stream, (
+        draft.data_ptr(), None if draft_prob is None else draft_prob.data_ptr(),
+        target_prob.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+        None if n_draft is None else n_draft.data_ptr(),
+        n_accept.data_ptr(), next_token.data_ptr(), B, b, V))
     if st != BD_OK:
         raise BdAttnError(st, "bd_spec_verify")
     return n_accept, next_token

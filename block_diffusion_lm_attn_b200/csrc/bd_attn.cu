@@ -976,12 +976,13 @@ bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
         return BD_ERR_INVALID_ARG;
     if (B <= 0 || b <= 0 || V <= 0)
         return BD_ERR_INVALID_ARG;
-    if (V > bd::kVerifyMaxVocab)
+    if (V > bd::kVerifyMaxVocab || B > INT_MAX / bd::kVerifyCluster)
         return BD_ERR_UNSUPPORTED;
     bd::VerifyParams p = {draft, draft_prob, target_prob, u_accept, u_sample, n_draft,
                           n_accept, next_token, B, b, V};
-    const int smem = (int)cdiv(V, bd::kVerifySeg) * (int)sizeof(double);
-    bd::bd_spec_verify_kernel<<<B, bd::kVerifyThreads, smem, stream>>>(p);
+    const int segs = (int)cdiv(V, bd::kVerifySeg * bd::kVerifyCluster); // per CTA
+    bd::bd_spec_verify_kernel<<<B * bd::kVerifyCluster, bd::kVerifyThreads,
+                                segs * sizeof(double), stream>>>(p, segs);
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 

@@ -11,16 +11,22 @@
 // Products of two floats are exact in double, so each acceptance is decided
 // exactly; the running sums are double too, added in a fixed order.
 //
-// Bound by reading one row of p and one of q per sequence (8 V bytes).
+// Bound by reading one row of p and one of q per sequence (8 V bytes), and for
+// few sequences by latency: the gathers of the acceptance, the rows, the entry
+// in its segment, each waits for the one before.  A cluster of 8 CTAs takes a
+// sequence, an eighth of the vocabulary each, and exchanges the eight sums
+// through shared memory; one CTA a sequence took 36 us for one sequence of
+// 50001 entries and 136 us for 64 of 131072.
 #pragma once
 
 #include "bd_common.cuh"
 
 namespace bd {
 
-constexpr int kVerifyThreads = 1024;
-constexpr int kVerifySeg = 1024;            // vocabulary entries per segment
-constexpr int kVerifyMaxVocab = 4096 * kVerifySeg;
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyCluster = 8;
+constexpr int kVerifySeg = 256; // vocabulary entries per segment: 8 a lane
+constexpr int kVerifyMaxVocab = 1 << 22;
 
 struct VerifyParams {
     const int32_t *draft;     // [B, b]
@@ -70,110 +76,191 @@ __device__ __forceinline__ int verify_accept(const VerifyParams &p, int i, int l
     return __any_sync(0xffffffffu, bad) ? -1 : n;
 }
 
-// One CTA per sequence.
-__global__ void __launch_bounds__(kVerifyThreads)
-    bd_spec_verify_kernel(const VerifyParams p)
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the double at `addr` of this CTA's shared memory, in CTA `rank` of the cluster
+__device__ __forceinline__ double cluster_ld(uint32_t addr, uint32_t rank)
+{
+    double v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.f64 %0, [a];\n\t}"
+                 : "=d"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+// sum over lanes 0 .. lane
+__device__ __forceinline__ double warp_scan(double v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += up;
+    }
+    return v;
+}
+
+// Cluster = sequence, CTA = a run of `segs` segments of the vocabulary.
+__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 2)
+    bd_spec_verify_kernel(const VerifyParams p, int segs)
 {
     extern __shared__ double seg[]; // sum of each segment's weights
+    __shared__ double s_total[2];   // this CTA's, of each pass
     __shared__ int s_n;
-    __shared__ int s_alive;
-    const int i = blockIdx.x;
+    const int i = blockIdx.x / kVerifyCluster, rank = blockIdx.x % kVerifyCluster;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
         const int n = verify_accept(p, i, lane);
         if (lane == 0) {
             s_n = n;
-            s_alive = 0;
-            if (n < 0)
-                raise_device_code(DEV_BAD_CACHE_LEN);
-            p.n_accept[i] = max(n, 0);
-            p.next_token[i] = -1;
+            if (rank == 0) {
+                if (n < 0) {
+                    raise_device_code(DEV_BAD_CACHE_LEN);
+                    p.next_token[i] = -1;
+                }
+                p.n_accept[i] = max(n, 0);
+            }
         }
     }
     __syncthreads();
     const int n = s_n;
-    if (n < 0)
+    if (n < 0) // in every CTA of the cluster
         return;
     const int nd = p.n_draft ? p.n_draft[i] : p.b;
     const float *pr = p.target_prob + ((size_t)i * (p.b + 1) + n) * p.V;
     const float *qr = n < nd && p.draft_prob ? p.draft_prob + ((size_t)i * p.b + n) * p.V : nullptr;
     const int point = n < nd && !p.draft_prob ? p.draft[(size_t)i * p.b + n] : -1;
-    const int segs = (p.V + kVerifySeg - 1) / kVerifySeg;
+    const int v0 = rank * segs * kVerifySeg; // this CTA's entries
+    const int v1 = min(p.V, v0 + segs * kVerifySeg);
+    const int mine = v1 > v0 ? (v1 - v0 + kVerifySeg - 1) / kVerifySeg : 0;
     bool residual = n < nd;
 
-    auto weight = [&](int t) -> double {
-        double w = pr[t];
-        if (residual)
-            w -= qr ? (double)qr[t] : (t == point ? 1.0 : 0.0);
-        return w > 0.0 ? w : 0.0;
+    constexpr int E = kVerifySeg / 32;
+    // weights of entries t + step * e; t's own bound is v1
+    auto weights = [&](int t, int step, double *w) {
+        float a[E], b[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const bool in = t + step * e < v1;
+            a[e] = in ? pr[t + step * e] : 0.f;
+            b[e] = in && residual && qr ? qr[t + step * e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (residual && t + step * e == point)
+                b[e] = 1.f;
+            const double x = (double)a[e] - (double)b[e];
+            w[e] = x > 0.0 ? x : 0.0; // NaN counts as 0
+        }
     };
-    for (;;) {
-        for (int g = warp; g < segs; g += kVerifyThreads / 32) {
+    double total = 0.0, before = 0.0; // of the cluster; of the CTAs before this one
+    int owner_last = -1;              // last CTA with mass
+    int pass = 0;
+    for (;; ++pass) {
+        for (int g = warp; g < mine; g += kVerifyThreads / 32) {
+            double w[E];
+            weights(v0 + g * kVerifySeg + lane, 32, w);
             double part = 0.0;
-#pragma unroll 8
-            for (int t = g * kVerifySeg + lane; t < min(p.V, (g + 1) * kVerifySeg); t += 32)
-                part += weight(t);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                part += w[e];
             part = warp_sum(part);
-            if (lane == 0) {
+            if (lane == 0)
                 seg[g] = part;
-                if (part > 0.0)
-                    s_alive = 1;
-            }
         }
         __syncthreads();
-        if (s_alive || !residual)
+        if (warp == 0) {
+            double sum = 0.0;
+            for (int g = lane; g < mine; g += 32)
+                sum += seg[g];
+            sum = warp_sum(sum);
+            if (lane == 0)
+                s_total[pass] = sum;
+        }
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+        const uint32_t addr = smem_u32(&s_total[pass]);
+        total = before = 0.0;
+#pragma unroll
+        for (int r = 0; r < kVerifyCluster; ++r) {
+            const double x = cluster_ld(addr, r);
+            if (r < rank)
+                before += x;
+            total += x;
+            if (x > 0.0)
+                owner_last = r;
+        }
+        if (total > 0.0 || !residual)
             break;
         residual = false; // nothing left of p - q: draw from p
-        __syncthreads();
     }
-    if (warp != 0 || !s_alive)
-        return;
-    double total = 0.0;
-    int last = 0; // last segment with mass
-    for (int g = 0; g < segs; ++g) {
-        total += seg[g];
-        if (seg[g] > 0.0)
-            last = g;
-    }
-    const double want = (double)p.u_sample[i] * total;
-    double before = 0.0;
-    int g = 0;
-    for (; g < last; ++g) {
-        if (before + seg[g] > want)
-            break;
-        before += seg[g];
-    }
-    // lane l takes entries 32 l .. 32 l + 31 of segment g
-    const int t0 = g * kVerifySeg + lane * 32, t1 = min(p.V, t0 + 32);
-    double mine = 0.0;
-    int last_pos = -1;
-    for (int t = t0; t < t1; ++t) {
-        const double w = weight(t);
-        mine += w;
-        if (w > 0.0)
-            last_pos = t;
-    }
-    double incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += up;
-    }
-    double run = before + (incl - mine);
-    int found = INT_MAX;
-    for (int t = t0; t < t1; ++t) {
-        const double w = weight(t);
-        run += w;
-        if (w > 0.0 && run > want) {
-            found = t;
-            break;
+    cluster_arrive(); // the sums have been read; waited for before the exit
+    // the CTA whose entries hold the drawn one: the first whose running sum
+    // passes `want`, or the last with mass
+    const double u = p.u_sample[i];
+    const double want = u > 0.0 ? u * total : 0.0; // (a NaN draws the first)
+    const double own = s_total[pass];
+    const bool here = own > 0.0 && before <= want && (before + own > want || rank == owner_last);
+    if (total <= 0.0 && rank == 0 && threadIdx.x == 0)
+        p.next_token[i] = -1;
+    if (warp == 0 && here) {
+        // the segment, 32 at a time
+        double run = before;
+        int g = -1, last = -1;
+        double at = 0.0, last_at = 0.0; // sum before segments g, last
+        for (int g0 = 0; g0 < mine && g < 0; g0 += 32) {
+            const double x = g0 + lane < mine ? seg[g0 + lane] : 0.0;
+            const double incl = run + warp_scan(x, lane);
+            const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && incl > want);
+            const unsigned mass = __ballot_sync(0xffffffffu, x > 0.0);
+            if (hit) {
+                g = g0 + __ffs(hit) - 1;
+                at = __shfl_sync(0xffffffffu, incl - x, __ffs(hit) - 1);
+            }
+            if (mass) {
+                last = g0 + 31 - __clz(mass);
+                last_at = __shfl_sync(0xffffffffu, incl - x, 31 - __clz(mass));
+            }
+            run = __shfl_sync(0xffffffffu, incl, 31);
         }
+        if (g < 0) {
+            g = last;
+            at = last_at;
+        }
+        // lane l takes entries E l .. E l + E - 1 of segment g
+        const int t0 = v0 + g * kVerifySeg + lane * E;
+        double w[E];
+        weights(t0, 1, w);
+        double sum = 0.0;
+        int last_pos = -1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            sum += w[e];
+            if (w[e] > 0.0)
+                last_pos = t0 + e;
+        }
+        double c = at + (warp_scan(sum, lane) - sum);
+        int found = INT_MAX;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            c += w[e];
+            if (w[e] > 0.0 && c > want && found == INT_MAX)
+                found = t0 + e;
+        }
+        found = __reduce_min_sync(0xffffffffu, found);
+        last_pos = __reduce_max_sync(0xffffffffu, last_pos);
+        if (lane == 0)
+            p.next_token[i] = found == INT_MAX ? last_pos : found;
     }
-    found = __reduce_min_sync(0xffffffffu, found);
-    last_pos = __reduce_max_sync(0xffffffffu, last_pos);
-    if (lane == 0)
-        p.next_token[i] = found == INT_MAX ? last_pos : found;
+    cluster_wait();
 }
 
 } // namespace bd

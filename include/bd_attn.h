@@ -543,7 +543,7 @@ BD_API bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache,
  * gets n_accept 0 and next_token -1, and the device status word records
  * BD_ERR_DEVICE_TIMEOUT.  Errors: BD_ERR_INVALID_ARG for a null or misaligned
  * pointer, a size <= 0 or one buffer for both outputs; BD_ERR_UNSUPPORTED for
- * V > 4194304; BD_ERR_CUDA if the launch fails.
+ * V > 4194304 or B > 268435455; BD_ERR_CUDA if the launch fails.
  */
 BD_API bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
                                 const float *target_prob, const float *u_accept,
