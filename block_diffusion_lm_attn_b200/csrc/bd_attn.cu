@@ -981,8 +981,15 @@ bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
     bd::VerifyParams p = {draft, draft_prob, target_prob, u_accept, u_sample, n_draft,
                           n_accept, next_token, B, b, V};
     const int segs = (int)cdiv(V, bd::kVerifySeg * bd::kVerifyCluster); // per CTA
-    bd::bd_spec_verify_kernel<<<B * bd::kVerifyCluster, bd::kVerifyThreads,
-                                segs * sizeof(double), stream>>>(p, segs);
+    // Few sequences: more threads to a CTA, for fewer rounds of loads.  Many:
+    // four smaller CTAs to an SM, so that 64 sequences run at once (with half
+    // the loads in flight, 64 of 131072 entries took 29 us with the small
+    // CTAs, 35 us with the large ones; one of 50001 8.8 us and 7.0 us).
+    const int grid = B * bd::kVerifyCluster, smem = segs * (int)sizeof(double);
+    if (grid <= 2 * kMaxGrid)
+        bd::bd_spec_verify_kernel<512><<<grid, 512, smem, stream>>>(p, segs);
+    else
+        bd::bd_spec_verify_kernel<256><<<grid, 256, smem, stream>>>(p, segs);
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 

@@ -71,10 +71,21 @@ __device__ __forceinline__ float exp2_int(int k) // -126 <= k <= 127
     return __uint_as_float((uint32_t)(k + 127) << 23);
 }
 
+__device__ __forceinline__ uint32_t umax_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // One CTA per (touched group, kv-head and K or V, sequence).  NV: vectors of
-// 8 values a thread, held in registers between the maximum and the codes.
+// 8 values a thread, held in registers between the maximum and the codes as
+// they were read (bf16, or codes of rows that stay): 4 registers a vector
+// where floats took 8, and so four CTAs to an SM where there were two.
+// Non-negative bf16 order as their bits do, so the maximum is taken on pairs
+// of 16 bits.
 template <int NV>
-__global__ void __launch_bounds__(kQ8Threads)
+__global__ void __launch_bounds__(kQ8Threads, 4)
     bd_cache_append_q8_kernel(const Q8Params p)
 {
     __shared__ float red[kQ8Threads / 32];
@@ -93,69 +104,104 @@ __global__ void __launch_bounds__(kQ8Threads)
     uint8_t *codes = (is_v ? p.v_cache : p.k_cache) + head * p.S_cap * p.d;
     float *scale = (is_v ? p.v_scale : p.k_scale) + head * p.groups + g;
     const bf16 *src = (is_v ? p.v_new : p.k_new) + head * p.b * p.d;
-    const int vpr = p.d / 8;            // vectors per row
+    const int vpr = p.d / 8; // vectors per row: a power of two
+    const int shift = 31 - __clz(vpr);
     const int total = p.T * vpr;
     const float old = *scale;
     const int row0 = g * p.T;
 
-    float x[NV][8];
-    float amax = 0.f;
+    uint4 w[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int e = v * blockDim.x + threadIdx.x;
-        const int row = row0 + e / vpr, col = (e % vpr) * 8;
+        const int row = row0 + (e >> shift), col = (e & (vpr - 1)) * 8;
+        w[v] = make_uint4(0, 0, 0, 0);
         if (e < total && row >= len && row < len + n) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + (size_t)(row - len) * p.d + col);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                x[v][2 * t] = __uint_as_float(ws[t] << 16);
-                x[v][2 * t + 1] = __uint_as_float(ws[t] & 0xffff0000u);
-            }
+            w[v] = *reinterpret_cast<const uint4 *>(src + (size_t)(row - len) * p.d + col);
         } else if (e < total && row < len) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(codes + (size_t)row * p.d + col);
-            const uint32_t ws[2] = {w.x, w.y};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float2 f = float2_of_e4m3x2((uint16_t)(ws[t >> 1] >> (16 * (t & 1))));
-                x[v][2 * t] = f.x * old;
-                x[v][2 * t + 1] = f.y * old;
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-                x[v][t] = 0.f;
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const float m = fabsf(x[v][t]);
-            amax = m < INFINITY ? fmaxf(amax, m) : amax; // finite values only
+            const uint2 c = *reinterpret_cast<const uint2 *>(codes + (size_t)row * p.d + col);
+            w[v].x = c.x;
+            w[v].y = c.y;
         }
     }
+    // the 8 values of vector v
+    auto values = [&](int v, bool kept, float *x) {
+        const uint32_t ws[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int t = 0; t < 4; ++t) {
+            if (kept) {
+                const float2 f = float2_of_e4m3x2((uint16_t)(ws[t >> 1] >> (16 * (t & 1))));
+                x[2 * t] = f.x * old;
+                x[2 * t + 1] = f.y * old;
+            } else {
+                x[2 * t] = __uint_as_float(ws[t] << 16);
+                x[2 * t + 1] = __uint_as_float(ws[t] & 0xffff0000u);
+            }
+        }
+    };
+    float amax = 0.f; // of the finite values
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        if (row0 + ((v * (int)blockDim.x + (int)threadIdx.x) >> shift) < len) {
+            float x[8];
+            values(v, true, x);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float m = fabsf(x[t]);
+                amax = m < INFINITY ? fmaxf(amax, m) : amax;
+            }
+        } else {
+            top = umax_u16x2(top, w[v].x & 0x7fff7fffu);
+            top = umax_u16x2(top, w[v].y & 0x7fff7fffu);
+            top = umax_u16x2(top, w[v].z & 0x7fff7fffu);
+            top = umax_u16x2(top, w[v].w & 0x7fff7fffu);
+        }
+    }
+    if ((top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u) {
+        top = 0; // an infinity or a NaN: once more, without them
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (row0 + ((v * (int)blockDim.x + (int)threadIdx.x) >> shift) < len)
+                continue;
+            float x[8];
+            values(v, false, x);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float m = fabsf(x[t]);
+                amax = m < INFINITY ? fmaxf(amax, m) : amax;
+            }
+        }
+    }
+    amax = fmaxf(amax, fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u)));
+    // non-negative floats order as their bits do
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
     if ((threadIdx.x & 31) == 0)
         red[threadIdx.x >> 5] = amax;
     __syncthreads(); // also: every thread has read the old scale
     amax = red[0];
-    for (int w = 1; w < (int)blockDim.x / 32; ++w)
-        amax = fmaxf(amax, red[w]);
+    for (int x = 1; x < (int)blockDim.x / 32; ++x)
+        amax = fmaxf(amax, red[x]);
     const int k = q8_scale_exp(amax);
     const float s = exp2_int(k), inv = exp2_int(-k);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int e = v * blockDim.x + threadIdx.x;
-        const int row = row0 + e / vpr, col = (e % vpr) * 8;
+        const int row = row0 + (e >> shift), col = (e & (vpr - 1)) * 8;
         // rows that stay keep their codes under the same scale
         if (e >= total || row >= len + n || (row < len && s == old))
             continue;
-        uint2 w;
-        w.x = (uint32_t)e4m3x2(x[v][0] * inv, x[v][1] * inv) |
-              (uint32_t)e4m3x2(x[v][2] * inv, x[v][3] * inv) << 16;
-        w.y = (uint32_t)e4m3x2(x[v][4] * inv, x[v][5] * inv) |
-              (uint32_t)e4m3x2(x[v][6] * inv, x[v][7] * inv) << 16;
-        *reinterpret_cast<uint2 *>(codes + (size_t)row * p.d + col) = w;
+        float x[8];
+        if (row < len)
+            values(v, true, x);
+        else
+            values(v, false, x);
+        uint2 c;
+        c.x = (uint32_t)e4m3x2(x[0] * inv, x[1] * inv) |
+              (uint32_t)e4m3x2(x[2] * inv, x[3] * inv) << 16;
+        c.y = (uint32_t)e4m3x2(x[4] * inv, x[5] * inv) |
+              (uint32_t)e4m3x2(x[6] * inv, x[7] * inv) << 16;
+        *reinterpret_cast<uint2 *>(codes + (size_t)row * p.d + col) = c;
     }
     if (threadIdx.x == 0)
         *scale = s;

@@ -71,6 +71,26 @@ __global__ void __launch_bounds__(kRopeThreads)
     const bool turn = u * 16 < p.rot;
     if (!turn && !p.copy)
         return;
+    // the two 16-byte chunks of the unit
+    const int a = INTERLEAVED || !turn ? u * 16 : u * 8;
+    const int b = INTERLEAVED || !turn ? u * 16 + 8 : p.rot / 2 + u * 8;
+    const int h0 = blockIdx.y * p.heads, h1 = min(h0 + p.heads, p.Hq + p.Hkv);
+    auto at = [&](int h) -> size_t {
+        const size_t hh = h < p.Hq ? (size_t)i * p.Hq + h : (size_t)i * p.Hkv + (h - p.Hq);
+        return (hh * p.N + n) * p.d;
+    };
+    constexpr int U = 4; // heads whose loads are in flight together
+    uint4 va[U], vb[U];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int w = 0; w < U; ++w)
+            if (h + w < h1) {
+                const bf16 *src = (h + w < p.Hq ? p.q : p.k) + at(h + w);
+                va[w] = *reinterpret_cast<const uint4 *>(src + a);
+                vb[w] = *reinterpret_cast<const uint4 *>(src + b);
+            }
+    };
+    load(h0); // on their way while the angles are taken
     float c[8], s[8];
     if (turn) {
         const long long pos = p.positions ? (long long)p.positions[(size_t)i * p.N + n]
@@ -84,24 +104,9 @@ __global__ void __launch_bounds__(kRopeThreads)
             s[e] *= p.mscale * p.sign;
         }
     }
-    // the two 16-byte chunks of the unit
-    const int a = INTERLEAVED || !turn ? u * 16 : u * 8;
-    const int b = INTERLEAVED || !turn ? u * 16 + 8 : p.rot / 2 + u * 8;
-    const int h0 = blockIdx.y * p.heads, h1 = min(h0 + p.heads, p.Hq + p.Hkv);
-    auto at = [&](int h) -> size_t {
-        const size_t hh = h < p.Hq ? (size_t)i * p.Hq + h : (size_t)i * p.Hkv + (h - p.Hq);
-        return (hh * p.N + n) * p.d;
-    };
-    constexpr int U = 4; // heads whose loads are in flight together
     for (int h = h0; h < h1; h += U) {
-        uint4 va[U], vb[U];
-#pragma unroll
-        for (int w = 0; w < U; ++w)
-            if (h + w < h1) {
-                const bf16 *src = (h + w < p.Hq ? p.q : p.k) + at(h + w);
-                va[w] = *reinterpret_cast<const uint4 *>(src + a);
-                vb[w] = *reinterpret_cast<const uint4 *>(src + b);
-            }
+        if (h != h0)
+            load(h);
 #pragma unroll
         for (int w = 0; w < U; ++w)
             if (h + w < h1) {

@@ -15,17 +15,19 @@
 // few sequences by latency: the gathers of the acceptance, the rows, the entry
 // in its segment, each waits for the one before.  A cluster of 8 CTAs takes a
 // sequence, an eighth of the vocabulary each, and exchanges the eight sums
-// through shared memory; one CTA a sequence took 36 us for one sequence of
-// 50001 entries and 136 us for 64 of 131072.
+// through shared memory; a lane has 32 loads in flight.  Measured: 7.8 us for
+// one sequence of 50001 entries (one CTA a sequence: 36), 15.7 us for 64 of
+// 131072 (137; 16 loads in flight: 29), 4.3 TB/s.
 #pragma once
+
+#include <limits.h>
 
 #include "bd_common.cuh"
 
 namespace bd {
 
-constexpr int kVerifyThreads = 512;
 constexpr int kVerifyCluster = 8;
-constexpr int kVerifySeg = 256; // vocabulary entries per segment: 8 a lane
+constexpr int kVerifySeg = 512; // vocabulary entries per segment: 16 a lane
 constexpr int kVerifyMaxVocab = 1 << 22;
 
 struct VerifyParams {
@@ -108,7 +110,8 @@ __device__ __forceinline__ double warp_scan(double v, int lane)
 }
 
 // Cluster = sequence, CTA = a run of `segs` segments of the vocabulary.
-__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 2)
+template <int THREADS>
+__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(THREADS, 1024 / THREADS)
     bd_spec_verify_kernel(const VerifyParams p, int segs)
 {
     extern __shared__ double seg[]; // sum of each segment's weights
@@ -143,34 +146,42 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
     bool residual = n < nd;
 
     constexpr int E = kVerifySeg / 32;
-    // weights of entries t + step * e; t's own bound is v1
-    auto weights = [&](int t, int step, double *w) {
+    // weights of entries t + step * e below v1, all of them if `full`
+    auto weights = [&](int t, int step, bool full, auto use) {
         float a[E], b[E];
+        const float *pt = pr + t, *qt = (residual && qr ? qr : pr) + t;
+        if (full) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const bool in = t + step * e < v1;
-            a[e] = in ? pr[t + step * e] : 0.f;
-            b[e] = in && residual && qr ? qr[t + step * e] : 0.f;
+            for (int e = 0; e < E; ++e)
+                a[e] = pt[step * e];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                b[e] = residual && qr ? qt[step * e] : 0.f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const bool in = t + step * e < v1;
+                a[e] = in ? pt[step * e] : 0.f;
+                b[e] = in && residual && qr ? qt[step * e] : 0.f;
+            }
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if (residual && t + step * e == point)
                 b[e] = 1.f;
-            const double x = (double)a[e] - (double)b[e];
-            w[e] = x > 0.0 ? x : 0.0; // NaN counts as 0
+            // NaN counts as 0; a > b decides, so the conversions of the
+            // others are of no consequence
+            use(e, a[e] > b[e] ? (double)a[e] - (double)b[e] : 0.0);
         }
     };
     double total = 0.0, before = 0.0; // of the cluster; of the CTAs before this one
     int owner_last = -1;              // last CTA with mass
     int pass = 0;
     for (;; ++pass) {
-        for (int g = warp; g < mine; g += kVerifyThreads / 32) {
-            double w[E];
-            weights(v0 + g * kVerifySeg + lane, 32, w);
+        for (int g = warp; g < mine; g += THREADS / 32) {
             double part = 0.0;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                part += w[e];
+            weights(v0 + g * kVerifySeg + lane, 32, v0 + (g + 1) * kVerifySeg <= v1,
+                    [&](int, double w) { part += w; });
             part = warp_sum(part);
             if (lane == 0)
                 seg[g] = part;
@@ -237,24 +248,20 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
         }
         // lane l takes entries E l .. E l + E - 1 of segment g
         const int t0 = v0 + g * kVerifySeg + lane * E;
-        double w[E];
-        weights(t0, 1, w);
         double sum = 0.0;
         int last_pos = -1;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            sum += w[e];
-            if (w[e] > 0.0)
+        weights(t0, 1, false, [&](int e, double w) {
+            sum += w;
+            if (w > 0.0)
                 last_pos = t0 + e;
-        }
+        });
         double c = at + (warp_scan(sum, lane) - sum);
         int found = INT_MAX;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            c += w[e];
-            if (w[e] > 0.0 && c > want && found == INT_MAX)
+        weights(t0, 1, false, [&](int e, double w) {
+            c += w;
+            if (w > 0.0 && c > want && found == INT_MAX)
                 found = t0 + e;
-        }
+        });
         found = __reduce_min_sync(0xffffffffu, found);
         last_pos = __reduce_max_sync(0xffffffffu, last_pos);
         if (lane == 0)
