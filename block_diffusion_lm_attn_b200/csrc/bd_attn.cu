@@ -8,7 +8,8 @@
 // which also runs block decode; the backward in attn_tc_bwd.cuh; the cache
 // and SPRINT kernels in cache_ops.cuh.  The serving step over a cache in 8
 // bits: rope.cuh (positions), cache_q8.cuh (writing and reading the cache),
-// attn_q8_tc.cuh (decode), spec_verify.cuh (verification).
+// attn_q8_tc.cuh and
+// attn_q8_rows.cuh (decode), spec_verify.cuh (verification).
 #include "bd_attn.h"
 #include "bd_attn_debug.h"
 
@@ -27,6 +28,7 @@
 #include "attn_tc_persist.cuh"
 #include "attn_tc_pair.cuh"
 #include "attn_tc_bwd.cuh"
+#include "attn_q8_rows.cuh"
 #include "attn_q8_tc.cuh"
 #include "bd_common.cuh"
 #include "cache_ops.cuh"
@@ -232,19 +234,24 @@ bool make_map_rows(CUtensorMap *m, const void *base, uint64_t n1, uint64_t n2,
     return r == CUDA_SUCCESS;
 }
 
-// 3-D map over e4m3 codes [n2][n1][d]: boxes of 128 codes x 128 rows x 1,
-// 128-byte swizzle; columns past d and rows past n1 read as zero.
-bool make_map_codes(CUtensorMap *m, const void *base, uint64_t n1, uint64_t n2, uint64_t d)
+// 3-D map over e4m3 codes [n2][n1][d]: boxes of box_cols codes x box_rows rows
+// x 1, swizzled over box_cols bytes (32, 64 or 128); columns past d and rows
+// past n1 read as zero.
+bool make_map_codes(CUtensorMap *m, const void *base, uint64_t n1, uint64_t n2, uint64_t d,
+                    uint32_t box_cols, uint32_t box_rows)
 {
     auto enc = tensor_map_encoder();
     if (!enc)
         return false;
     cuuint64_t dims[3] = {d, n1, n2};
     cuuint64_t strides[2] = {d, d * n1};
-    cuuint32_t box[3] = {128, 128, 1};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_cols == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+               : box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : CU_TENSOR_MAP_SWIZZLE_32B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -405,6 +412,9 @@ inline bool aligned4(const void *p)
 // Group sizes of a cache in 8 bits: whole 16-key chunks of a key tile.
 inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
 
+// Query rows of a unit up to which the kernel for few rows takes it.
+constexpr int kQ8FewRows = 32;
+
 template <int DH>
 bd_status launch_q8_tc(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
                        int grid, cudaStream_t st)
@@ -413,6 +423,35 @@ bd_status launch_q8_tc(const CUtensorMap &mk, const CUtensorMap &mv, const bd::Q
         return BD_ERR_CUDA;
     bd::bd_decode_q8_tc_kernel<DH><<<grid, bd::kQtThreads, bd::kQtSmemBytes, st>>>(mk, mv, p);
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
+template <int DH, int MT>
+bd_status launch_q8_rows(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
+                         int grid, cudaStream_t st)
+{
+    constexpr int smem = bd::kQrSmemBytes;
+    if (set_smem<bd::bd_decode_q8_rows_kernel<DH, MT>>(smem) != BD_OK)
+        return BD_ERR_CUDA;
+    bd::bd_decode_q8_rows_kernel<DH, MT><<<grid, bd::kQrThreads, smem, st>>>(mk, mv, p);
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
+// The 8-bit decode's attention kernel for these rows per unit.
+template <int DH>
+bd_status launch_q8(const void *k_cache, const void *v_cache, const bd::QtParams &p, int grid,
+                    cudaStream_t st)
+{
+    const bool rows = p.pp.rows_unit <= kQ8FewRows;
+    const uint32_t cols = rows ? DH : 128, keys = rows ? bd::kQrTile / DH : 128;
+    CUtensorMap mk, mv;
+    const uint64_t heads = (uint64_t)p.pp.B * p.pp.Hkv;
+    if (!make_map_codes(&mk, k_cache, (uint64_t)p.pp.nkeys, heads, DH, cols, keys) ||
+        !make_map_codes(&mv, v_cache, (uint64_t)p.pp.nkeys, heads, DH, cols, keys))
+        return BD_ERR_CUDA;
+    if (!rows)
+        return launch_q8_tc<DH>(mk, mv, p, grid, st);
+    return p.pp.rows_unit <= 16 ? launch_q8_rows<DH, 1>(mk, mv, p, grid, st)
+                                : launch_q8_rows<DH, 2>(mk, mv, p, grid, st);
 }
 
 // Host-side checks shared by the calls on a cache in 8 bits.
@@ -950,14 +989,10 @@ bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache, const void *
     p.vs = v_scale;
     p.groups = (int)cdiv(S_cap, group);
     p.tshift = group == 16 ? 4 : group == 32 ? 5 : group == 64 ? 6 : 7;
-    CUtensorMap mk, mv;
-    if (!make_map_codes(&mk, k_cache, (uint64_t)S_cap, (uint64_t)B * Hkv, d) ||
-        !make_map_codes(&mv, v_cache, (uint64_t)S_cap, (uint64_t)B * Hkv, d))
-        return BD_ERR_CUDA;
     const int G = persistent_grid();
-    st = d == 128  ? launch_q8_tc<128>(mk, mv, p, G, stream)
-         : d == 64 ? launch_q8_tc<64>(mk, mv, p, G, stream)
-                   : launch_q8_tc<32>(mk, mv, p, G, stream);
+    st = d == 128  ? launch_q8<128>(k_cache, v_cache, p, G, stream)
+         : d == 64 ? launch_q8<64>(k_cache, v_cache, p, G, stream)
+                   : launch_q8<32>(k_cache, v_cache, p, G, stream);
     return st == BD_OK ? launch_combine<true>(p.pp, G, stream) : st;
 }
 

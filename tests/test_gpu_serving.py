@@ -316,6 +316,30 @@ def test_decode_head_groups_and_block_sizes(Hq, H, b):
         run_decode(q, kv, lens, mode, 32)
 
 
+@pytest.mark.parametrize("d,group", [(128, 64), (128, 16), (64, 128), (64, 32), (32, 16), (32, 128)])
+@pytest.mark.parametrize("Hq,H,b", [(4, 1, 1), (3, 1, 5), (4, 2, 8), (4, 1, 5), (8, 2, 8), (1, 1, 31)])
+def test_decode_few_rows(Hq, H, b, d, group):
+    """Up to 16 and up to 32 query rows a unit, over prefixes that end inside
+    and at the end of a step, a part of one and a run of 16 keys."""
+    for mode in (0, 1, 2):
+        lens = [1, 33, 128, 255, 1100, 0 if mode == 2 else 64]
+        q, kv = decode_case(len(lens), Hq, H, b, d, 1200, group, lens, mode, 100 * Hq + 10 * b + d + mode)
+        run_decode(q, kv, lens, mode, group)
+
+
+@pytest.mark.parametrize("rows", [(4, 1, 1), (8, 2, 7)])
+@pytest.mark.parametrize("grid", [1, 2, 5, 31])
+def test_decode_few_rows_split_over_any_grid(grid, rows):
+    Hq, H, b = rows
+    lens = [2500, 3, 700, 0, 129, 1]
+    q, kv = decode_case(6, Hq, H, b, 128, 2600, 64, lens, 1, grid)
+    assert bd.bd_attn_debug_set_grid(grid) == bd.BD_OK
+    try:
+        run_decode(q, kv, lens, 1, 64)
+    finally:
+        bd.bd_attn_debug_set_grid(0)
+
+
 @pytest.mark.parametrize("grid", [1, 3, 5, 37])
 def test_decode_split_over_any_grid(grid):
     lens = [1500, 3, 700, 0, 129]
@@ -354,6 +378,26 @@ def test_decode_groups_of_very_different_scale():
     run_decode(q, [(kc, ks), (vc, vs)], lens, 0, 32)
 
 
+def test_decode_few_rows_sharp_scores_and_scales():
+    """One row per head: rows of different size, value groups 2^40 apart, a
+    group of zeros, scales that are no powers of two."""
+    lens = [700]
+    q, kv = decode_case(1, 8, 2, 1, 128, 800, 32, lens, 1, 85)
+    q[0, 0] = 0
+    q[0, 1] *= 2.0 ** -20
+    q[0, 2] *= 64
+    q[0, 3, 0, 5] = 200.0
+    q[0, 4] *= 2.0 ** -100
+    run_decode(q, kv, lens, 1, 32)
+    (kc, ks), (vc, vs) = kv
+    vs[0, :, 1] *= 2.0 ** 20
+    vs[0, :, 2] *= 2.0 ** -20
+    vc[0, :, 96:160] = 0
+    vs[0, :, 3:5] = 2.0 ** -64
+    ks = ks * (0.7 + torch.rand(ks.shape, generator=gen(86)))
+    run_decode(q, [(kc, ks), (vc, vs)], lens, 1, 32)
+
+
 def test_decode_any_positive_scale():
     lens = [200, 77]
     q, kv = decode_case(2, 4, 2, 5, 128, 220, 16, lens, 0, 79)
@@ -377,6 +421,29 @@ def test_decode_not_a_number():
     want[0, 0, 1] = want[0, 0, 2] = want[0, 1, 2] = want[0, 1, 3] = True
     assert torch.equal(nan, want)
     assert torch.equal(torch.isnan(out).all(-1).cpu(), want) and torch.equal(torch.isnan(out).any(-1).cpu(), want)
+
+
+@pytest.mark.parametrize("b", [1, 40])
+@pytest.mark.parametrize("grid", [1, 7])
+def test_decode_not_a_number_in_a_cut_unit(b, grid):
+    """The same where a unit's pieces are merged, and for few rows."""
+    lens = [1000]
+    q, kv = decode_case(1, 2, 1, b, 128, 1100, 16, lens, 0, 84)
+    q[0, 0, 0, 9] = float("-inf")
+    (kc, ks), (vc, vs) = kv
+    assert bd.bd_attn_debug_set_grid(grid) == bd.BD_OK
+    try:
+        out, lse = bd.decode_q8(q.cuda(), cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 0, 16)
+        ok()
+        want = torch.zeros((1, 2, b), dtype=torch.bool)
+        want[0, 0, 0] = True
+        assert torch.equal(torch.isnan(lse).cpu(), want) and torch.equal(torch.isnan(out).any(-1).cpu(), want)
+        kc[0, 0, 700, 3] = 0x7f  # a key that every row sees
+        out, lse = bd.decode_q8(q.cuda(), cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 0, 16)
+        ok()
+        assert torch.isnan(lse).all() and torch.isnan(out).all()
+    finally:
+        bd.bd_attn_debug_set_grid(0)
 
 
 def test_decode_bad_length_is_reported():
