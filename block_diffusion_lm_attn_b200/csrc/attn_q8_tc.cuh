@@ -262,6 +262,26 @@ __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint3
     return finite ? exp2_int(k) : NAN;
 }
 
+// Bounded wait by a converged warp, as mbar_wait_warp, with one vote a poll and
+// no divergent path in between: the kernel waits about 20 times a tile.
+__device__ __forceinline__ bool qt_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1))
+        return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, BD_WAIT_SLEEP_NS)))
+            return true;
+        if (__any_sync(0xffffffffu, *abort_flag))
+            return false;
+        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) {
+            *abort_flag = 1;
+            raise_device_code(DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 template <int DH>
 __global__ void __launch_bounds__(kQtThreads, 1)
     bd_decode_q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -273,28 +293,28 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     uint8_t *sbase = smem_raw + (base - raw_addr);
 
     const uint32_t bar0 = base + kQtSmemBar;
-    auto bar_kfull = [&](int s) { return bar0 + 8 * s; };
+    // What the MMAs of a tile wait for arrives on one barrier each: for the QK
+    // of tile j, K and the reads of S of tile j - 1; for its PVs, P of both
+    // warpgroups and V in f16.
+    auto bar_qk = [&](int s) { return bar0 + 8 * s; };          // tile j & 3
     auto bar_kempty = [&](int s) { return bar0 + 32 + 8 * s; };
     auto bar_vfull = [&](int s) { return bar0 + 64 + 8 * s; };
     auto bar_vempty = [&](int s) { return bar0 + 96 + 8 * s; };
     auto bar_ifull = [&](int s) { return bar0 + 128 + 8 * s; }; // segment si & 3
     auto bar_iempty = [&](int s) { return bar0 + 160 + 8 * s; };
-    const uint32_t bar_sread = bar0 + 192; // S read by both warpgroups
-    const uint32_t bar_qfull = bar0 + 200;
-    const uint32_t bar_qfree = bar0 + 208; // last QK of a segment done
-    auto bar_pfull = [&](int w) { return bar0 + 224 + 8 * w; }; // P of warpgroup w
-    auto bar_odone = [&](int w) { return bar0 + 240 + 8 * w; }; // its PV done
-    auto bar_w = [&](int s) { return bar0 + 256 + 8 * s; };     // V of tile j & 1 in f16
-    auto bar_wfree = [&](int s) { return bar0 + 272 + 8 * s; }; // both its PVs done
+    auto bar_pv = [&](int s) { return bar0 + 192 + 8 * s; };    // tile j & 1
+    auto bar_odone = [&](int s) { return bar0 + 208 + 8 * s; }; // PVs of tile j & 1 done
     // S of tile j & 1, its scales and those of the queries: one buffer of S,
     // but the converters arrive up to a tile ahead
-    auto bar_sfull = [&](int s) { return bar0 + 312 + 8 * s; };
-    const uint32_t bar_l = bar0 + 288;     // both sums of a segment written
-    const uint32_t bar_ofree = bar0 + 296; // both O read out
-    const uint32_t bar_final = bar0 + 304;
+    auto bar_sfull = [&](int s) { return bar0 + 224 + 8 * s; };
+    const uint32_t bar_qfull = bar0 + 240;
+    const uint32_t bar_qfree = bar0 + 248; // last QK of a segment done
+    const uint32_t bar_l = bar0 + 256;     // both sums of a segment written
+    const uint32_t bar_ofree = bar0 + 264; // both O read out
+    const uint32_t bar_final = bar0 + 272;
     static_assert(kQtKStages == 4 && kQtVStages == 4, "barrier layout");
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 336);
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 344);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 288);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 296);
     Seg *seg_ring = reinterpret_cast<Seg *>(sbase + kQtSmemSeg); // nt = 0: no more
     float2 *s_l = reinterpret_cast<float2 *>(sbase + kQtSmemL);
     float *s_qs = reinterpret_cast<float *>(sbase + kQtSmemQs);
@@ -305,21 +325,18 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 4; ++s) {
-            mbar_init(bar_kfull(s), 1);
+            mbar_init(bar_qk(s), 1 + 8); // TMA, softmax warps
             mbar_init(bar_kempty(s), 1);
             mbar_init(bar_vfull(s), 1 + 2 * kQtChunks); // + a copy of each scale
-            mbar_init(bar_vempty(s), 4);
+            mbar_init(bar_vempty(s), 3);
             mbar_init(bar_ifull(s), 1);
             mbar_init(bar_iempty(s), 14); // 8 softmax warps, MMA, V, 4 converters
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar_pfull(s), 4);
+            mbar_init(bar_pv(s), 8 + 3); // softmax warps, converters
             mbar_init(bar_odone(s), 1);
-            mbar_init(bar_w(s), 4);
-            mbar_init(bar_wfree(s), 1);
             mbar_init(bar_sfull(s), 5); // the MMA, 4 converters
         }
-        mbar_init(bar_sread, 8);
         mbar_init(bar_qfull, 4);
         mbar_init(bar_qfree, 1);
         mbar_init(bar_l, 256);
@@ -344,7 +361,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // a barrier wait by a converged warp
-    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort_flag); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return qt_wait(bar, parity, abort_flag); };
 
     if (warp == 8) {
         // ------------------------------------------ work list, loads of K
@@ -384,9 +401,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 const bool skip = g == 0 && blockIdx.x == 0 && lane == 0 &&
                                   atomicExch(&g_fault_skip_k, 0) != 0;
                 if (lane == 0 && !skip) {
-                    mbar_expect_tx(bar_kfull(s), kQtTile);
+                    mbar_expect_tx(bar_qk(s), kQtTile);
                     tma_load_3d(base + kQtSmemK + s * kQtTile, &tm_k, 0, sg.lo0 + it * kTcN, sg.kvhead,
-                                bar_kfull(s));
+                                bar_qk(s));
                     kiss = g + 1;
                 }
                 __syncwarp();
@@ -396,7 +413,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         if (lane == 0) {
             const long long c0 = clock64();
             for (int x = kiss > 4 ? kiss - 4 : 0; x < kiss; ++x)
-                while (!mbar_try_wait(bar_kfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
+                while (!mbar_try_wait(bar_qk(x & 3), (uint32_t)((x >> 2) & 1)) &&
                        clock64() - c0 < kWaitCycles) {}
         }
     } else if (warp == 10) {
@@ -468,8 +485,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 ++qs;
             }
             const int s = qj & 3;
-            if (!(ok = wait(bar_kfull(s), (uint32_t)((qj >> 2) & 1))) ||
-                (qj >= 1 && !(ok = wait(bar_sread, (uint32_t)((qj - 1) & 1)))))
+            if (!(ok = wait(bar_qk(s), (uint32_t)((qj >> 2) & 1))))
                 return;
             tc_fence_after();
             const uint32_t kb = base + kQtSmemK + (uint32_t)s * kQtTile;
@@ -495,27 +511,23 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 const int b = j & 1;
                 // O was last read out by the epilogue of segment si - 1
                 if (!ok || (i == 0 && si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1)))) ||
-                    !(ok = wait(bar_w(b), (uint32_t)((j >> 1) & 1))))
+                    !(ok = wait(bar_pv(b), (uint32_t)((j >> 1) & 1))))
                     break;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = wait(bar_pfull(half), (uint32_t)(j & 1))))
-                        break;
-                    tc_fence_after();
-                    const uint32_t vb = base + kQtSmemW + (uint32_t)b * kTileBytes + half * (kQtStep * 128);
-                    // (the last tile may have no key in its second half)
-                    if (half == 0 || i * kTcN + kQtStep < hi) {
+                tc_fence_after();
+                const uint32_t vb = base + kQtSmemW + (uint32_t)b * kTileBytes;
 #pragma unroll
-                        for (int kk = 0; kk < kQtStep / 16; ++kk)
-                            tc_mma_ts_p(t_o + half * 128, t_p + half * 32 + kk * 8,
-                                        smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024),
-                                        idesc_pv, (i > 0 || kk > 0) ? 1u : 0u, ld);
-                    }
-                    tc_commit_p(bar_odone(half), ld);
+                for (int half = 0; half < 2; ++half) {
+                    // (the last tile may have no key in its second half)
+                    if (half == 1 && i * kTcN + kQtStep >= hi)
+                        break;
+#pragma unroll
+                    for (int kk = 0; kk < kQtStep / 16; ++kk)
+                        tc_mma_ts_p(t_o + half * 128, t_p + half * 32 + kk * 8,
+                                    smem_desc_sw128(vb + half * (kQtStep * 128) + kk * 2048,
+                                                    kHalfTileBytes, 1024),
+                                    idesc_pv, (i > 0 || kk > 0) ? 1u : 0u, ld);
                 }
-                if (!ok)
-                    break;
-                tc_commit_p(bar_wfree(b), ld);
+                tc_commit_p(bar_odone(b), ld);
             }
             __syncwarp();
             if (ok && lane == 0)
@@ -570,12 +582,12 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 break;
             for (int it = 0; it < nt; ++it, ++j) {
                 const int s = j & 3, ks = lo + it * kTcN;
-                if (!(ok = wait(bar_vfull(s), (uint32_t)((j >> 2) & 1))))
+                if (cw != 1 && !(ok = wait(bar_vfull(s), (uint32_t)((j >> 2) & 1))))
                     break;
                 // the f16 buffer was last read by the PVs of tile j - 2;
                 // the softmax of that tile lies behind them
                 const int b = j & 1;
-                if (j >= 2 && !(ok = wait(bar_wfree(b), (uint32_t)(((j - 2) >> 1) & 1))))
+                if (j >= 2 && !(ok = wait(bar_odone(b), (uint32_t)(((j - 2) >> 1) & 1))))
                     break;
                 if (cw == 0) {
                     if (lane < kQtChunks) {
@@ -602,42 +614,51 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 const int r8 = (lane & 4) ? (hrow ^ 5) : hrow;
                 const int u4 = lane & 3;
                 constexpr int H = DH <= 64 ? 1 : 2; // halves of 64 columns
-                // warp cw: rows 32 cw .. 32 cw + 31; all loads go out first
-                uint32_t x[4 * H][4];
+                // 16 rows at a time: warps 12, 14, 15 take 6, 4 and 6 such
+                // pairs of 8; warp 13 shares its scheduler with the MMA warp
+                // and takes none
+                if (cw == 1)
+                    continue;
+                const int row0 = cw == 0 ? 0 : cw == 2 ? 48 : 80;
+                const int row1 = cw == 0 ? 48 : cw == 2 ? 80 : 128;
+#pragma unroll 1
+                for (int rr = row0; rr < row1; rr += 16) {
+                    uint32_t x[2 * H][4];
 #pragma unroll
-                for (int i = 0; i < 4 * H; ++i) {
-                    const int r = 32 * cw + 8 * (i / H) + r8;
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
-                                 : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
-                                 : "memory");
-                }
-                if (ks + 32 * cw + 32 > hi) { // not keys: no code of theirs may be used
+                    for (int i = 0; i < 2 * H; ++i) {
+                        const int r = rr + 8 * (i / H) + r8;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
+                                     : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
+                                     : "memory");
+                    }
+                    if (ks + rr + 16 > hi) { // not keys: no code of theirs may be used
 #pragma unroll
-                    for (int i = 0; i < 4 * H; ++i)
-                        if (ks + 32 * cw + 8 * (i / H) + r8 >= hi)
-                            x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
-                }
+                        for (int i = 0; i < 2 * H; ++i)
+                            if (ks + rr + 8 * (i / H) + r8 >= hi)
+                                x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
+                    }
 #pragma unroll
-                for (int i = 0; i < 4 * H; ++i) {
-                    uint32_t y[8];
+                    for (int i = 0; i < 2 * H; ++i) {
+                        uint32_t y[8];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        y[t] = half2_of_e4m3x2((uint16_t)(x[i][t >> 1] >> (16 * (t & 1))));
-                    const uint32_t row = dst + (i % H) * kHalfTileBytes + (32 * cw + 8 * (i / H) + r8) * 128;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     row + (((2 * u4) ^ r8) << 4)),
-                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     row + (((2 * u4 + 1) ^ r8) << 4)),
-                                 "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                                 : "memory");
+                        for (int t = 0; t < 8; ++t)
+                            y[t] = half2_of_e4m3x2((uint16_t)(x[i][t >> 1] >> (16 * (t & 1))));
+                        const uint32_t row = dst + (i % H) * kHalfTileBytes + (rr + 8 * (i / H) + r8) * 128;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         row + (((2 * u4) ^ r8) << 4)),
+                                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         row + (((2 * u4 + 1) ^ r8) << 4)),
+                                     "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                                     : "memory");
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(bar_w(b));
+                    mbar_arrive(bar_pv(b));
                     mbar_arrive(bar_vempty(s));
                 }
             }
@@ -654,6 +675,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         const uint32_t lane_off = (uint32_t)wrow << 16;
         const uint32_t ts = tmem + wg * kQtStep + lane_off; // its half of S
         const uint32_t t_ow = t_o + wg * 128 + lane_off; // this warpgroup's O
+        if (lane == 0)
+            mbar_arrive(bar_qk(0)); // no S before tile 0
         bool ok = true;
         int j0 = 0; // tile of the CTA at the segment's start
         for (int si = 0; ok; ++si) {
@@ -668,31 +691,22 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             // keys that this row sees
             const int seen = min(hi, sg.len + (p.pp.mode == 0 ? p.pp.b : p.pp.mode == 1 ? jr + 1 : 0));
             const bool live = wrow < nrows; // a warp without rows only arrives
-            float qs = 1.f;
+            // tiles in which this warp has rows and keys: all of them, or all but
+            // the last, or none
+            const int n_own = live ? (hi - lo + kTcN - 1 - wg * kQtStep) / kTcN : 0;
             float m = -INFINITY, l = 0.f; // running maximum (raised lazily), sum
-            for (int i = 0; i < n; ++i) {
+            for (int i = 0; i < n_own; ++i) {
                 const int j = j0 + i; // tile
                 const int ks = lo + i * kTcN + wg * kQtStep;
                 if (!(ok = wait(bar_sfull(j & 1), (uint32_t)((j >> 1) & 1))))
                     break;
-                if (!live || ks >= hi) { // no rows, or (in the last tile) no keys
-                    if (lane == 0)
-                        mbar_arrive(bar_sread);
-                    if (j >= 1 && !(ok = wait(bar_odone(wg), (uint32_t)((j - 1) & 1))))
-                        break;
-                    if (lane == 0)
-                        mbar_arrive(bar_pfull(wg));
-                    continue;
-                }
-                if (i == 0)
-                    qs = s_qs[(si & 1) * kTcM + row];
                 tc_fence_after();
                 uint32_t sr[kQtStep];
                 tmem_ld32x2_wait(ts, ts + 32, sr, sr + 32);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar_sread);
+                    mbar_arrive(bar_qk((j + 1) & 3));
                 float s[kQtStep];
 #pragma unroll
                 for (int c = 0; c < kQtStep; ++c)
@@ -708,6 +722,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
                 constexpr int C = kQtStep / 16;
                 const float4 *tab = s_tab + (j & 3) * kQtChunks + wg * C;
+                const float qs = s_qs[(si & 1) * kTcM + row];
                 float4 e[C];
                 float mt = -INFINITY;
 #pragma unroll
@@ -730,7 +745,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         m = mt - kQtTop;
                     }
                     if (i > 0) { // the TMEM read-modify-write of O is warp-collective
-                        if (!(ok = wait(bar_odone(wg), (uint32_t)((j - 1) & 1))))
+                        if (!(ok = wait(bar_odone((j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1))))
                             break;
                         tc_fence_after();
 #pragma unroll 1
@@ -762,7 +777,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     l = fmaf(r0 + r1, e[c].z, l);
                 }
                 // P of the tile before has been used
-                if (j >= 1 && !(ok = wait(bar_odone(wg), (uint32_t)((j - 1) & 1))))
+                if (j >= 1 && !(ok = wait(bar_odone((j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1))))
                     break;
                 tc_fence_after();
                 tmem_st32(t_p + wg * 32 + lane_off, pk);
@@ -770,17 +785,26 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar_pfull(wg));
+                    mbar_arrive(bar_pv(j & 1));
+            }
+            for (int i = n_own; ok && i < n; ++i) { // only the arrivals
+                const int j = j0 + i;
+                if (!(ok = wait(bar_sfull(j & 1), (uint32_t)((j >> 1) & 1))))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive(bar_qk((j + 1) & 3));
+                    mbar_arrive(bar_pv(j & 1));
+                }
             }
             if (!ok)
                 break;
             const int jl = j0 + n - 1; // last tile of the segment
             s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float2(l, m);
             mbar_arrive(bar_l);
-            // both warpgroups' last PVs
+            // The last PVs.  (The phase before on that barrier is behind QK_jl,
+            // which this warp has seen.)
             if (!(ok = wait(bar_l, (uint32_t)(si & 1))) ||
-                !(ok = wait(bar_odone(0), (uint32_t)(jl & 1))) ||
-                !(ok = wait(bar_odone(1), (uint32_t)(jl & 1))))
+                !(ok = wait(bar_odone(jl & 1), (uint32_t)((jl >> 1) & 1))))
                 break;
             tc_fence_after();
             // factors of the two O to the common maximum; O_1 is unwritten
