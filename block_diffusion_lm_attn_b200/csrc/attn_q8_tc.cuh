@@ -16,22 +16,24 @@
 // Persistent, one CTA per SM, over units of a sequence, a kv-head and 128
 // query rows: whole ones, or equal ranges of 128-key tiles whose pieces
 // bd_decode_stream_combine_kernel merges (QtSource).  Roles:
-//   warps 0-3, 4-7  softmax, thread = query row = TMEM lane; one warpgroup
-//                   takes the first 64 keys of every tile, one the last
-//   warp 8          the work list, TMA of K
-//   warp 9          MMA issue: the QK of a tile, then the PVs of the tile
-//                   before, over segment boundaries
-//   warp 10         TMA of V, cp.async of the scales
-//   warps 12-15     V codes to f16; the table of scales; at the end of a
-//                   segment the next one's queries
-// TMEM: S of one tile (128 columns), P of the two halves (f16, 32 each), an O
-// for each warpgroup (128 each), Q (hi and lo, 32 each).
+//   warps 0-3, 4-7  softmax, thread = query row = TMEM lane; the warpgroups
+//                   take alternate key tiles, and the one without a segment's
+//                   last tile splits the next segment's queries meanwhile
+//   warp 8          the work list, TMA of K and V, cp.async of the scales
+//   warp 9          MMA issue: per tile its PV and the QK two tiles on
+//   warps 10, 11    V codes to f16
+// TMEM: S/P of even and of odd tiles (128 columns; P, f16, over its own S), an
+// O for each warpgroup (128).  Shared memory: Q (hi and lo, 16 KB each), four
+// stages of K and three of V (16 KB), two buffers of V in f16 (32 KB).
 //
-// A warpgroup reads its half of S into registers at once, so the next tile's
-// QK runs under its exponentials, and keeps an O, a running maximum and a sum
-// of its own: the two meet only in the epilogue, which joins them.  (With one
-// O and the maximum handed from step to step a step took 2500 cycles, a third
-// of them for the hand-over and the wait for S.)
+// Each warpgroup has an O, a running maximum and a sum of its own, joined in
+// the epilogue, so that a tile costs a softmax warp one wait (for S) and one
+// arrival (of P).  That count is what bounds the kernel: between two waits a
+// warp issues an instruction every 5 cycles or so, and a hand-over from warp to
+// warp costs some 200.  Forms that shared every tile between the warpgroups, 64
+// keys each, took 2850 cycles a tile (two waits and two arrivals a warp, the
+// scales of 64 keys against those of 128), with one O and a maximum handed from
+// warpgroup to warpgroup 3200.
 #pragma once
 
 #include "attn_tc_persist.cuh"
@@ -39,20 +41,17 @@
 
 namespace bd {
 
-constexpr int kQtThreads = 512;
-
+constexpr int kQtThreads = 384;
 constexpr int kQtTile = kTcN * kTcD; // bytes of a key tile's codes
-constexpr int kQtKStages = 4, kQtVStages = 4;
-constexpr int kQtChunks = kTcN / 16; // runs of 16 keys: one scale each
-constexpr int kQtStep = 64;          // keys per softmax step: two steps a tile
+constexpr int kQtKStages = 4, kQtVStages = 3;
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
-constexpr int kQtSmemK = 0;
+constexpr int kQtSmemQ = 0; // hi, lo
+constexpr int kQtSmemK = kQtSmemQ + 2 * kQtTile;
 constexpr int kQtSmemV = kQtSmemK + kQtKStages * kQtTile;
 constexpr int kQtSmemW = kQtSmemV + kQtVStages * kQtTile; // V in f16: 2 buffers
-constexpr int kQtSmemRaw = kQtSmemW + 2 * kTileBytes;     // scales, 16 a stage
-constexpr int kQtSmemTab = kQtSmemRaw + kQtVStages * 64;  // 4 tables of 8 float4
-constexpr int kQtSmemL = kQtSmemTab + 4 * kQtChunks * 16; // (l, M) [2][2][128]
+constexpr int kQtSmemSc = kQtSmemW + 2 * kTileBytes; // 8 tiles: 8 scales of K, 8 of V
+constexpr int kQtSmemL = kQtSmemSc + 8 * 64;         // (l, M) [2][2][128]
 constexpr int kQtSmemQs = kQtSmemL + 4 * kTcM * 8;        // row scales of Q [2][128]
 constexpr int kQtSmemSeg = kQtSmemQs + 2 * kTcM * 4;      // 4 segments, 128 B each
 constexpr int kQtSmemBar = kQtSmemSeg + 4 * 128;
@@ -171,15 +170,15 @@ struct QtParams {
     int groups, tshift;   // log2 of the positions per group
 };
 
-// D[tmem] (+)= A[tmem] * B[smem desc] of e4m3 codes
-__device__ __forceinline__ void tc_mma8_ts_p(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+// D[tmem] (+)= A[smem desc] * B[smem desc] of e4m3 codes
+__device__ __forceinline__ void tc_mma8_ss_p(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                              uint32_t idesc, uint32_t accumulate, uint32_t leader)
 {
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
                  "setp.ne.b32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
                  : "memory");
 }
 
@@ -217,15 +216,29 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
                  : "memory");
 }
 
-// A query row as two halves of e4m3 codes, and its scale.
-template <int DH>
-__device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint32_t *hi, uint32_t *lo)
+// 16 columns of tensor memory, with their wait
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t a0, uint32_t *r)
 {
-    const uint4 *row = reinterpret_cast<const uint4 *>(src);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+                 "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                   "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(a0)
+                 : "memory");
+}
+
+// A query row (thread = row) as two halves of e4m3 codes, hi and lo, in the
+// 128-byte swizzle of 128-byte rows at `dst` and `dst` + kQtTile; returns the
+// row's scale.
+template <int DH>
+__device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint32_t dst, int row)
+{
     uint4 w[DH / 8];
 #pragma unroll
     for (int i = 0; i < DH / 8; ++i)
-        w[i] = valid ? row[i] : make_uint4(0, 0, 0, 0);
+        w[i] = valid ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
     float amax = 0.f;
     bool finite = true;
 #pragma unroll
@@ -243,21 +256,31 @@ __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint3
     const int k = max(q8_scale_exp(finite ? amax : 0.f), -100);
     const float inv = finite ? exp2_int(-k) : NAN;
 #pragma unroll
-    for (int i = 0; i < DH / 8; ++i) {
-        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t h[4], r[4];
+    for (int c = 0; c < DH / 16; ++c) { // 16 codes of each half
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float a = __uint_as_float(ws[t] << 16) * inv;
-            const float b = __uint_as_float(ws[t] & 0xffff0000u) * inv;
-            h[t] = e4m3x2(a, b);
-            const float2 f = float2_of_e4m3x2((uint16_t)h[t]);
-            r[t] = e4m3x2(a - f.x, b - f.y);
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = w[2 * c + i];
+            const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4], r[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float a = __uint_as_float(ws[t] << 16) * inv;
+                const float b = __uint_as_float(ws[t] & 0xffff0000u) * inv;
+                h[t] = e4m3x2(a, b);
+                const float2 f = float2_of_e4m3x2((uint16_t)h[t]);
+                r[t] = e4m3x2(a - f.x, b - f.y);
+            }
+            hi[2 * i] = h[0] | h[1] << 16;
+            hi[2 * i + 1] = h[2] | h[3] << 16;
+            lo[2 * i] = r[0] | r[1] << 16;
+            lo[2 * i + 1] = r[2] | r[3] << 16;
         }
-        hi[2 * i] = h[0] | h[1] << 16;
-        hi[2 * i + 1] = h[2] | h[3] << 16;
-        lo[2 * i] = r[0] | r[1] << 16;
-        lo[2 * i + 1] = r[2] | r[3] << 16;
+        const uint32_t at = dst + row * 128 + ((c ^ (row & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]),
+                     "r"(hi[2]), "r"(hi[3]) : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + kQtTile), "r"(lo[0]),
+                     "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
     }
     return finite ? exp2_int(k) : NAN;
 }
@@ -282,7 +305,8 @@ __device__ __forceinline__ bool qt_wait(uint32_t bar, uint32_t parity, volatile 
     }
 }
 
-template <int DH>
+// NG: scales a tile has of K and of V each, 128 / (positions per group).
+template <int DH, int NG>
 __global__ void __launch_bounds__(kQtThreads, 1)
     bd_decode_q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const QtParams p)
@@ -293,52 +317,46 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     uint8_t *sbase = smem_raw + (base - raw_addr);
 
     const uint32_t bar0 = base + kQtSmemBar;
-    // What the MMAs of a tile wait for arrives on one barrier each: for the QK
-    // of tile j, K and the reads of S of tile j - 1; for its PVs, P of both
-    // warpgroups and V in f16.
-    auto bar_qk = [&](int s) { return bar0 + 8 * s; };          // tile j & 3
+    auto bar_kfull = [&](int s) { return bar0 + 8 * s; };
     auto bar_kempty = [&](int s) { return bar0 + 32 + 8 * s; };
     auto bar_vfull = [&](int s) { return bar0 + 64 + 8 * s; };
-    auto bar_vempty = [&](int s) { return bar0 + 96 + 8 * s; };
-    auto bar_ifull = [&](int s) { return bar0 + 128 + 8 * s; }; // segment si & 3
-    auto bar_iempty = [&](int s) { return bar0 + 160 + 8 * s; };
-    auto bar_pv = [&](int s) { return bar0 + 192 + 8 * s; };    // tile j & 1
-    auto bar_odone = [&](int s) { return bar0 + 208 + 8 * s; }; // PVs of tile j & 1 done
-    // S of tile j & 1, its scales and those of the queries: one buffer of S,
-    // but the converters arrive up to a tile ahead
-    auto bar_sfull = [&](int s) { return bar0 + 224 + 8 * s; };
-    const uint32_t bar_qfull = bar0 + 240;
-    const uint32_t bar_qfree = bar0 + 248; // last QK of a segment done
-    const uint32_t bar_l = bar0 + 256;     // both sums of a segment written
-    const uint32_t bar_ofree = bar0 + 264; // both O read out
-    const uint32_t bar_final = bar0 + 272;
-    static_assert(kQtKStages == 4 && kQtVStages == 4, "barrier layout");
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 288);
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 296);
+    auto bar_vempty = [&](int s) { return bar0 + 88 + 8 * s; };
+    auto bar_ifull = [&](int s) { return bar0 + 112 + 8 * s; };  // segment si & 3
+    auto bar_iempty = [&](int s) { return bar0 + 144 + 8 * s; };
+    auto bar_sfull = [&](int w) { return bar0 + 176 + 8 * w; };  // S of tile j & 1
+    auto bar_pv = [&](int w) { return bar0 + 192 + 8 * w; };     // its P, its V in f16
+    auto bar_odone = [&](int w) { return bar0 + 208 + 8 * w; };  // its PV done
+    auto bar_qfull = [&](int s) { return bar0 + 224 + 8 * s; };  // queries of segment si & 1
+    const uint32_t bar_l = bar0 + 240;     // both sums of a segment written
+    const uint32_t bar_ofree = bar0 + 248; // both O read out
+    const uint32_t bar_final = bar0 + 256;
+    static_assert(kQtKStages == 4 && kQtVStages == 3, "barrier layout");
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 272);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 280);
     Seg *seg_ring = reinterpret_cast<Seg *>(sbase + kQtSmemSeg); // nt = 0: no more
     float2 *s_l = reinterpret_cast<float2 *>(sbase + kQtSmemL);
     float *s_qs = reinterpret_cast<float *>(sbase + kQtSmemQs);
-    float4 *s_tab = reinterpret_cast<float4 *>(sbase + kQtSmemTab);
-    const float *s_raw = reinterpret_cast<const float *>(sbase + kQtSmemRaw);
+    const float *s_sc = reinterpret_cast<const float *>(sbase + kQtSmemSc);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 4; ++s) {
-            mbar_init(bar_qk(s), 1 + 8); // TMA, softmax warps
+            mbar_init(bar_kfull(s), 1 + 2 * NG); // + a copy of each scale
             mbar_init(bar_kempty(s), 1);
-            mbar_init(bar_vfull(s), 1 + 2 * kQtChunks); // + a copy of each scale
-            mbar_init(bar_vempty(s), 3);
             mbar_init(bar_ifull(s), 1);
-            mbar_init(bar_iempty(s), 14); // 8 softmax warps, MMA, V, 4 converters
+            mbar_init(bar_iempty(s), 11); // 8 softmax warps, MMA, 2 converters
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(bar_pv(s), 8 + 3); // softmax warps, converters
-            mbar_init(bar_odone(s), 1);
-            mbar_init(bar_sfull(s), 5); // the MMA, 4 converters
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(bar_vfull(s), 1);
+            mbar_init(bar_vempty(s), 2);
         }
-        mbar_init(bar_qfull, 4);
-        mbar_init(bar_qfree, 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(bar_sfull(w), 1);
+            mbar_init(bar_pv(w), 4 + 2); // softmax warps, converters
+            mbar_init(bar_odone(w), 1);
+            mbar_init(bar_qfull(w), 4);
+        }
         mbar_init(bar_l, 256);
         mbar_init(bar_ofree, 8);
         mbar_init(bar_final, 1);
@@ -355,7 +373,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t t_p = tmem + 128, t_o = tmem + 192, t_q = tmem + 448;
+    const uint32_t t_o = tmem + 256;
     // the combine kernel may be scheduled now; it reads nothing of this
     // launch before the whole grid has finished
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -364,20 +382,16 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     auto wait = [&](uint32_t bar, uint32_t parity) { return qt_wait(bar, parity, abort_flag); };
 
     if (warp == 8) {
-        // ------------------------------------------ work list, loads of K
+        // -------------------------- work list; loads of K, V and the scales
         QtSource src;
         src.init(p.pp);
         if (lane == 0)
             p.pp.cut_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-        // an empty range (more CTAs than tiles) contributes an empty piece
-        // to any cut unit that spans it
-        if (src.t0 == src.t1)
-            for (int r = lane; r < kTcM; r += 32)
-                p.pp.part_lse[(size_t)blockIdx.x * 2 * kTcM + r] = -INFINITY;
         Seg sg;
         bool ok = true;
-        int g = 0; // running tile counter
-        int kiss = 0;
+        int g = 0, vs = 0;           // running tile counter, its V stage
+        uint32_t vpar = 1;           // parity of the wait for that stage
+        int kiss = 0, viss = 0;      // tiles issued
         for (int si = 0; ok; ++si) {
             const int slot = si & 3;
             if (si >= 4 && !(ok = wait(bar_iempty(slot), (uint32_t)(((si - 4) >> 2) & 1))))
@@ -394,75 +408,57 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             if (!got)
                 break;
             for (int it = 0; it < sg.nt; ++it, ++g) {
-                const int s = g & 3;
+                const int ks = sg.lo0 + it * kTcN, s = g & 3;
                 if (g >= 4 && !(ok = wait(bar_kempty(s), (uint32_t)((g >> 2) & 1) ^ 1u)))
                     break;
                 // injected fault: this tile never arrives
                 const bool skip = g == 0 && blockIdx.x == 0 && lane == 0 &&
                                   atomicExch(&g_fault_skip_k, 0) != 0;
                 if (lane == 0 && !skip) {
-                    mbar_expect_tx(bar_qk(s), kQtTile);
-                    tma_load_3d(base + kQtSmemK + s * kQtTile, &tm_k, 0, sg.lo0 + it * kTcN, sg.kvhead,
-                                bar_qk(s));
+                    mbar_expect_tx(bar_kfull(s), kQtTile);
+                    tma_load_3d(base + kQtSmemK + s * kQtTile, &tm_k, 0, ks, sg.kvhead, bar_kfull(s));
                     kiss = g + 1;
                 }
+                // Scales: one lane each, K's first.  Groups with no visible key
+                // give 0, which no visible score is multiplied by.  A slot is
+                // taken again 8 tiles on, behind QK_{g-4} and so behind the
+                // softmax of tile g - 6.
+                if (lane < 2 * NG) {
+                    const int key = ks + (kTcN / NG) * (lane % NG);
+                    const bool in = key < sg.hi0;
+                    const float *from = (lane < NG ? p.ks : p.vs) + (size_t)sg.kvhead * p.groups +
+                                        (in ? key / (kTcN / NG) : 0);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                     base + kQtSmemSc + (g & 7) * 64 + (lane / NG) * 32 + (lane % NG) * 4),
+                                 "l"(from), "r"(in ? 4 : 0)
+                                 : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                                     bar_kfull(s))
+                                 : "memory");
+                }
+                if (g >= kQtVStages && !(ok = wait(bar_vempty(vs), vpar)))
+                    break;
+                if (lane == 0) {
+                    mbar_expect_tx(bar_vfull(vs), kQtTile);
+                    tma_load_3d(base + kQtSmemV + vs * kQtTile, &tm_v, 0, ks, sg.kvhead, bar_vfull(vs));
+                    viss = g + 1;
+                }
                 __syncwarp();
+                if (++vs == kQtVStages) {
+                    vs = 0;
+                    vpar ^= 1;
+                }
             }
         }
         // wait (bounded) for every copy this role issued
-        if (lane == 0) {
-            const long long c0 = clock64();
-            for (int x = kiss > 4 ? kiss - 4 : 0; x < kiss; ++x)
-                while (!mbar_try_wait(bar_qk(x & 3), (uint32_t)((x >> 2) & 1)) &&
-                       clock64() - c0 < kWaitCycles) {}
-        }
-    } else if (warp == 10) {
-        // ------------------------------------- loads of V and the scales
-        bool ok = true;
-        int g = 0, viss = 0;
-        for (int si = 0; ok; ++si) {
-            if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
-                break;
-            const Seg &sg = seg_ring[si & 3];
-            const int nt = sg.nt, lo = sg.lo0, hi = sg.hi0, head = sg.kvhead;
-            __syncwarp();
-            if (nt == 0)
-                break;
-            if (lane == 0)
-                mbar_arrive(bar_iempty(si & 3));
-            for (int it = 0; it < nt; ++it, ++g) {
-                const int ks = lo + it * kTcN;
-                const int s = g & 3;
-                if (g >= 4 && !(ok = wait(bar_vempty(s), (uint32_t)((g >> 2) & 1) ^ 1u)))
-                    break;
-                if (lane == 0) {
-                    mbar_expect_tx(bar_vfull(s), kQtTile);
-                    tma_load_3d(base + kQtSmemV + s * kQtTile, &tm_v, 0, ks, head, bar_vfull(s));
-                    viss = g + 1;
-                }
-                // lanes 0-7: scales of K, 8-15: of V; chunks with no visible
-                // key read nothing
-                if (lane < 2 * kQtChunks) {
-                    const int key = ks + 16 * (lane & 7);
-                    const bool in = key < hi;
-                    const float *src = (lane < 8 ? p.ks : p.vs) + (size_t)head * p.groups +
-                                       (in ? key >> p.tshift : 0);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                     base + kQtSmemRaw + s * 64 + lane * 4),
-                                 "l"(src), "r"(in ? 4 : 0)
-                                 : "memory");
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                                     bar_vfull(s))
-                                 : "memory");
-                }
-                __syncwarp();
-            }
-        }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0) {
             const long long c0 = clock64();
-            for (int x = viss > 4 ? viss - 4 : 0; x < viss; ++x)
-                while (!mbar_try_wait(bar_vfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
+            for (int x = max(kiss - kQtKStages, 0); x < kiss; ++x)
+                while (!mbar_try_wait(bar_kfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
+                       clock64() - c0 < kWaitCycles) {}
+            for (int x = max(viss - kQtVStages, 0); x < viss; ++x)
+                while (!mbar_try_wait(bar_vfull(x % kQtVStages), (uint32_t)((x / kQtVStages) & 1)) &&
                        clock64() - c0 < kWaitCycles) {}
         }
     } else if (warp == 9) {
@@ -472,62 +468,55 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         // O has DH columns; a 64-column half of V at least
         constexpr uint32_t idesc_pv = idesc_fmt0(kTcM, DH > 64 ? 128 : 64, 1);
         bool ok = true;
-        // cursor of the QKs: tile qj of the CTA, tile qi of the qn of its segment qs
-        int qj = 0, qi = 0, qn = 0, qs = 0;
-        auto next_qk = [&]() { // the next tile's QK, if there is one
-            if (qi == qn) {
-                if (!(ok = wait(bar_ifull(qs & 3), (uint32_t)((qs >> 2) & 1))))
-                    return;
-                qn = seg_ring[qs & 3].nt;
-                qi = 0;
-                if (qn == 0 || !(ok = wait(bar_qfull, (uint32_t)(qs & 1))))
-                    return;
-                ++qs;
-            }
-            const int s = qj & 3;
-            if (!(ok = wait(bar_qk(s), (uint32_t)((qj >> 2) & 1))))
-                return;
-            tc_fence_after();
-            const uint32_t kb = base + kQtSmemK + (uint32_t)s * kQtTile;
+        // K of tile j is there
+        auto have_k = [&](int j) { return ok = wait(bar_kfull(j & 3), (uint32_t)((j >> 2) & 1)); };
+        // QK of tile j.  Its S buffer held P of tile j - 2, whose PV was
+        // issued before.
+        auto qk = [&](int j) {
+            const uint32_t ts = tmem + (uint32_t)(j & 1) * kTcN;
+            const uint32_t qb = base + kQtSmemQ, kb = base + kQtSmemK + (uint32_t)(j & 3) * kQtTile;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int kk = 0; kk < DH / 32; ++kk)
-                    tc_mma8_ts_p(tmem, t_q + h * 32 + kk * 8, smem_desc_sw128(kb + kk * 32, 16, 1024),
-                                 idesc_qk, h || kk ? 1u : 0u, ld);
-            tc_commit_p(bar_sfull(qj & 1), ld);
-            tc_commit_p(bar_kempty(s), ld);
-            ++qj;
-            if (++qi == qn)
-                tc_commit_p(bar_qfree, ld);
+                    tc_mma8_ss_p(ts, smem_desc_sw128(qb + h * kQtTile + kk * 32, 16, 1024),
+                                 smem_desc_sw128(kb + kk * 32, 16, 1024), idesc_qk,
+                                 h || kk ? 1u : 0u, ld);
+            tc_commit_p(bar_sfull(j & 1), ld);
+            tc_commit_p(bar_kempty(j & 3), ld);
         };
-        next_qk();
-        int j = 0; // tile of the PVs
-        for (int si = 0; ok && j < qj; ++si) {
-            // known, as its first QK was issued
-            const int n = seg_ring[si & 3].nt, hi = seg_ring[si & 3].hi0 - seg_ring[si & 3].lo0;
-            for (int i = 0; i < n; ++i, ++j) {
-                next_qk();
-                const int b = j & 1;
-                // O was last read out by the epilogue of segment si - 1
-                if (!ok || (i == 0 && si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1)))) ||
-                    !(ok = wait(bar_pv(b), (uint32_t)((j >> 1) & 1))))
+        int j = 0;
+        for (int si = 0; ok; ++si) {
+            if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
+                break;
+            const int n = seg_ring[si & 3].nt;
+            if (n == 0 || !(ok = wait(bar_qfull(si & 1), (uint32_t)((si >> 1) & 1))))
+                break;
+            for (int i = 0; i < min(n, 2); ++i) {
+                if (!have_k(j + i))
                     break;
                 tc_fence_after();
-                const uint32_t vb = base + kQtSmemW + (uint32_t)b * kTileBytes;
+                qk(j + i);
+            }
+            // O was last read out by the epilogue of segment si - 1
+            if (!ok || (si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1)))))
+                break;
+            for (int i = 0; i < n; ++i, ++j) {
+                const int w = j & 1;
+                // (K first: it has been there for long, and nothing is to stand
+                // between the PV and the QK behind it)
+                if ((i + 2 < n && !have_k(j + 2)) || !(ok = wait(bar_pv(w), (uint32_t)((j >> 1) & 1))))
+                    break;
+                tc_fence_after();
+                const uint32_t vb = base + kQtSmemW + (uint32_t)w * kTileBytes;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    // (the last tile may have no key in its second half)
-                    if (half == 1 && i * kTcN + kQtStep >= hi)
-                        break;
-#pragma unroll
-                    for (int kk = 0; kk < kQtStep / 16; ++kk)
-                        tc_mma_ts_p(t_o + half * 128, t_p + half * 32 + kk * 8,
-                                    smem_desc_sw128(vb + half * (kQtStep * 128) + kk * 2048,
-                                                    kHalfTileBytes, 1024),
-                                    idesc_pv, (i > 0 || kk > 0) ? 1u : 0u, ld);
-                }
-                tc_commit_p(bar_odone(b), ld);
+                for (int kk = 0; kk < kTcN / 16; ++kk)
+                    tc_mma_ts_p(t_o + w * 128, tmem + w * kTcN + kk * 8,
+                                smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024), idesc_pv,
+                                (i > 1 || kk > 0) ? 1u : 0u, ld);
+                tc_commit_p(bar_odone(w), ld);
+                if (i + 2 < n)
+                    qk(j + 2);
             }
             __syncwarp();
             if (ok && lane == 0)
@@ -537,109 +526,57 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         const long long c0 = clock64();
         while (!mbar_try_wait(bar_final, 0) && clock64() - c0 < kWaitCycles) {}
         __syncwarp();
-    } else if (warp >= 12) {
-        // ------- V codes to f16, the table of scales, the split of queries
-        const int cw = warp - 12;
-        const int row = 32 * cw + lane;
-        // The queries of segment si; the buffer was last read by the QKs of
-        // the segment before.
-        auto split = [&](int si) -> bool {
-            if (!wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1)))
-                return false;
-            const Seg &sg = seg_ring[si & 3];
-            if (sg.nt == 0)
-                return true;
-            uint32_t hi[DH / 4], lo[DH / 4];
-            const float qs =
-                qt_split_row<DH>(p.q + ((size_t)sg.out_row0 + row) * DH, row < sg.nrows, hi, lo);
-            // behind the last QK of segment si - 1, which was issued behind
-            // the reads of every earlier segment's S and row scales
-            if (si >= 1 && !wait(bar_qfree, (uint32_t)((si - 1) & 1)))
-                return false;
-            s_qs[(si & 1) * kTcM + row] = qs;
-            tc_fence_after();
-            const uint32_t tq = t_q + ((uint32_t)(32 * cw) << 16);
-#pragma unroll
-            for (int c = 0; c < DH / 32; ++c) {
-                tmem_st8(tq + 8 * c, hi + 8 * c);
-                tmem_st8(tq + 32 + 8 * c, lo + 8 * c);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_qfull);
-            return true;
-        };
-        bool ok = split(0);
-        int j = 0;
+    } else if (warp >= 10) {
+        // ------------------------------------------------ V codes to f16
+        const int cw = warp - 10;
+        bool ok = true;
+        int j = 0, vs = 0;
+        uint32_t vpar = 0;
         for (int si = 0; ok; ++si) {
             if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
                 break;
             const Seg &sg = seg_ring[si & 3];
             const int nt = sg.nt, lo = sg.lo0, hi = sg.hi0;
+            __syncwarp();
             if (nt == 0)
                 break;
+            if (lane == 0)
+                mbar_arrive(bar_iempty(si & 3));
             for (int it = 0; it < nt; ++it, ++j) {
-                const int s = j & 3, ks = lo + it * kTcN;
-                if (cw != 1 && !(ok = wait(bar_vfull(s), (uint32_t)((j >> 2) & 1))))
+                const int b = j & 1, ks = lo + it * kTcN;
+                // the f16 buffer was last read by the PV of tile j - 2
+                if (!(ok = wait(bar_vfull(vs), vpar)) ||
+                    (j >= 2 && !(ok = wait(bar_odone(b), (uint32_t)(((j - 2) >> 1) & 1)))))
                     break;
-                // the f16 buffer was last read by the PVs of tile j - 2;
-                // the softmax of that tile lies behind them
-                const int b = j & 1;
-                if (j >= 2 && !(ok = wait(bar_odone(b), (uint32_t)(((j - 2) >> 1) & 1))))
-                    break;
-                if (cw == 0) {
-                    if (lane < kQtChunks) {
-                        float4 e = make_float4(1.f, 0.f, 0.f, 0.f);
-                        if (ks + 16 * lane < hi) {
-                            const float sv = s_raw[s * 16 + 8 + lane];
-                            e.x = s_raw[s * 16 + lane] * p.pp.scale_log2;
-                            e.y = lg2(sv);
-                            e.z = 1.f / sv;
-                        }
-                        s_tab[(j & 3) * kQtChunks + lane] = e;
-                    }
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_sfull(b));
                 // 8 lanes take half a row each of rows r and r ^ 5 (64 codes
                 // = 4 vectors of 16): their reads of the swizzled codes and
                 // their writes of the swizzled halves each cover all banks.
-                const uint32_t src = base + kQtSmemV + (uint32_t)s * kQtTile;
+                const uint32_t src = base + kQtSmemV + (uint32_t)vs * kQtTile;
                 const uint32_t dst = base + kQtSmemW + (uint32_t)b * kTileBytes;
                 // rows of 8: pairs (0, 5), (2, 7), (4, 1), (6, 3)
                 const int hrow = (lane >> 3) * 2;
                 const int r8 = (lane & 4) ? (hrow ^ 5) : hrow;
                 const int u4 = lane & 3;
                 constexpr int H = DH <= 64 ? 1 : 2; // halves of 64 columns
-                // 16 rows at a time: warps 12, 14, 15 take 6, 4 and 6 such
-                // pairs of 8; warp 13 shares its scheduler with the MMA warp
-                // and takes none
-                if (cw == 1)
-                    continue;
-                const int row0 = cw == 0 ? 0 : cw == 2 ? 48 : 80;
-                const int row1 = cw == 0 ? 48 : cw == 2 ? 80 : 128;
 #pragma unroll 1
-                for (int rr = row0; rr < row1; rr += 16) {
-                    uint32_t x[2 * H][4];
+                for (int rr = 64 * cw; rr < 64 * cw + 64; rr += 32) {
+                    uint32_t x[4 * H][4]; // all loads go out first
 #pragma unroll
-                    for (int i = 0; i < 2 * H; ++i) {
+                    for (int i = 0; i < 4 * H; ++i) {
                         const int r = rr + 8 * (i / H) + r8;
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
                                      : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
                                      : "memory");
                     }
-                    if (ks + rr + 16 > hi) { // not keys: no code of theirs may be used
+                    if (ks + rr + 32 > hi) { // not keys: no code of theirs may be used
 #pragma unroll
-                        for (int i = 0; i < 2 * H; ++i)
+                        for (int i = 0; i < 4 * H; ++i)
                             if (ks + rr + 8 * (i / H) + r8 >= hi)
                                 x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
                     }
 #pragma unroll
-                    for (int i = 0; i < 2 * H; ++i) {
+                    for (int i = 0; i < 4 * H; ++i) {
                         uint32_t y[8];
 #pragma unroll
                         for (int t = 0; t < 8; ++t)
@@ -659,158 +596,178 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar_pv(b));
-                    mbar_arrive(bar_vempty(s));
+                    mbar_arrive(bar_vempty(vs));
+                }
+                if (++vs == kQtVStages) {
+                    vs = 0;
+                    vpar ^= 1;
                 }
             }
-            __syncwarp();
-            if (ok && lane == 0)
-                mbar_arrive(bar_iempty(si & 3));
-            ok = ok && split(si + 1);
         }
-    } else if (warp < 8) {
+    } else {
         // ------------------------------------------- softmax and epilogue
         const int wg = warp >> 2;
         const int row = threadIdx.x & (kTcM - 1);
         const int wrow = row & ~31; // first row of this warp
         const uint32_t lane_off = (uint32_t)wrow << 16;
-        const uint32_t ts = tmem + wg * kQtStep + lane_off; // its half of S
-        const uint32_t t_ow = t_o + wg * 128 + lane_off; // this warpgroup's O
-        if (lane == 0)
-            mbar_arrive(bar_qk(0)); // no S before tile 0
-        bool ok = true;
+        const uint32_t ts = tmem + wg * kTcN + lane_off;   // this warpgroup's S
+        const uint32_t t_ow = t_o + wg * 128 + lane_off;   // and O
+        // The queries of segment si, by one warpgroup, into the buffer that
+        // no QK reads any more.
+        auto split = [&](int si) -> bool {
+            if (!wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1)))
+                return false;
+            const Seg &sg = seg_ring[si & 3];
+            if (sg.nt == 0)
+                return true;
+            s_qs[(si & 1) * kTcM + row] = qt_split_row<DH>(
+                p.q + ((size_t)sg.out_row0 + row) * DH, row < sg.nrows, base + kQtSmemQ, row);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_qfull(si & 1));
+            return true;
+        };
+        bool ok = wg == 0 || split(0);
         int j0 = 0; // tile of the CTA at the segment's start
         for (int si = 0; ok; ++si) {
             if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
                 break;
             const Seg &sg = seg_ring[si & 3];
-            if (sg.nt == 0)
+            const int n = sg.nt;
+            if (n == 0)
                 break;
-            const int n = sg.nt, nrows = sg.nrows, lo = sg.lo0, hi = sg.hi0;
+            if (!(ok = wait(bar_qfull(si & 1), (uint32_t)((si >> 1) & 1))))
+                break;
+            const float qs = s_qs[(si & 1) * kTcM + row] * p.pp.scale_log2;
+            const int nrows = sg.nrows, lo = sg.lo0, hi = sg.hi0;
             const int full_end = min(sg.fhi0, hi); // keys that every row sees
             const int jr = (sg.qrow0 + min(row, nrows - 1)) % p.pp.b;
             // keys that this row sees
             const int seen = min(hi, sg.len + (p.pp.mode == 0 ? p.pp.b : p.pp.mode == 1 ? jr + 1 : 0));
             const bool live = wrow < nrows; // a warp without rows only arrives
-            // tiles in which this warp has rows and keys: all of them, or all but
-            // the last, or none
-            const int n_own = live ? (hi - lo + kTcN - 1 - wg * kQtStep) / kTcN : 0;
             float m = -INFINITY, l = 0.f; // running maximum (raised lazily), sum
-            for (int i = 0; i < n_own; ++i) {
+            for (int i = (j0 ^ wg) & 1; i < n; i += 2) {
                 const int j = j0 + i; // tile
-                const int ks = lo + i * kTcN + wg * kQtStep;
-                if (!(ok = wait(bar_sfull(j & 1), (uint32_t)((j >> 1) & 1))))
+                if (!(ok = wait(bar_sfull(wg), (uint32_t)((j >> 1) & 1))))
                     break;
-                tc_fence_after();
-                uint32_t sr[kQtStep];
-                tmem_ld32x2_wait(ts, ts + 32, sr, sr + 32);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_qk((j + 1) & 3));
-                float s[kQtStep];
+                if (live) {
+                    tc_fence_after();
+                    uint32_t sr[kTcN];
+                    tmem_ld32x4_wait(ts, ts + 32, ts + 64, ts + 96, sr, sr + 32, sr + 64, sr + 96);
+                    float s[kTcN];
 #pragma unroll
-                for (int c = 0; c < kQtStep; ++c)
-                    s[c] = __uint_as_float(sr[c]);
-                if (ks + kQtStep > full_end) {
+                    for (int c = 0; c < kTcN; ++c)
+                        s[c] = __uint_as_float(sr[c]);
+                    const int ks = lo + i * kTcN;
+                    if (ks + kTcN > full_end) {
 #pragma unroll
-                    for (int w = 0; w < kQtStep / 32; ++w) {
-                        const uint32_t mk = range_bits(0, seen - ks - 32 * w);
+                        for (int w = 0; w < kTcN / 32; ++w) {
+                            const uint32_t mk = range_bits(0, seen - ks - 32 * w);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            s[32 * w + c] = ((mk >> c) & 1u) ? s[32 * w + c] : -INFINITY;
-                    }
-                }
-                constexpr int C = kQtStep / 16;
-                const float4 *tab = s_tab + (j & 3) * kQtChunks + wg * C;
-                const float qs = s_qs[(si & 1) * kTcM + row];
-                float4 e[C];
-                float mt = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const float *x = s + 16 * c;
-                    const float m0 = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
-                    const float m1 = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
-                    e[c] = tab[c];
-                    // the product is no less than 2^-126: a masked score has
-                    // to stay -inf (and below that x is 0 anyway)
-                    e[c].x = fmaxf(e[c].x * qs, 1.2e-38f);
-                    mt = fmaxf(mt, fmaf(fmaxf(m0, m1), e[c].x, e[c].y));
-                }
-                const bool need = mt > m + (kQtTop + kQtLazy);
-                if (__any_sync(0xffffffffu, need)) {
-                    float c = 1.f;
-                    if (need) {
-                        c = m == -INFINITY ? 0.f : ex2(m - (mt - kQtTop));
-                        l = m == -INFINITY ? l : l * c; // 0, or NaN for good
-                        m = mt - kQtTop;
-                    }
-                    if (i > 0) { // the TMEM read-modify-write of O is warp-collective
-                        if (!(ok = wait(bar_odone((j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1))))
-                            break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q4 = 0; q4 < DH / 32; ++q4) {
-                            uint32_t o[32];
-                            tmem_ld32_wait(t_ow + q4 * 32, o);
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                o[x] = __float_as_uint(__uint_as_float(o[x]) * c);
-                            tmem_st32(t_ow + q4 * 32, o);
+                            for (int c = 0; c < 32; ++c)
+                                s[32 * w + c] = ((mk >> c) & 1u) ? s[32 * w + c] : -INFINITY;
                         }
                     }
-                }
-                const float nm = m == -INFINITY ? 0.f : -m;
-                uint32_t pk[kQtStep / 2];
+                    // the scales, as the multiplier of the scores and as the
+                    // term that P has from V; a masked score has to stay -inf,
+                    // so the product is no less than 2^-126 (where x is 0
+                    // anyway)
+                    float ea[NG], ev[NG];
+                    const float *sc = s_sc + (j & 7) * 16;
+                    float mt = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const float o = e[c].y + nm;
-                    float r0 = 0.f, r1 = 0.f;
+                    for (int c = 0; c < NG; ++c) {
+                        const bool in = ks + c * (kTcN / NG) < hi;
+                        ea[c] = fmaxf(sc[c] * qs, 1.2e-38f);
+                        ev[c] = in ? sc[8 + c] : 1.f;
+                        const float *x = s + c * (kTcN / NG);
+                        float mc[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
 #pragma unroll
-                    for (int x = 16 * c; x < 16 * c + 16; x += 2) {
-                        float y0, y1;
-                        ffma2(y0, y1, s[x], s[x + 1], e[c].x, e[c].x, o, o);
-                        y0 = ex2(y0);
-                        y1 = ex2(y1);
-                        fadd2(r0, r1, r0, r1, y0, y1);
-                        pk[x / 2] = pack_f16x2(y0, y1);
+                        for (int y = 4; y < kTcN / NG; y += 4) {
+                            mc[0] = fmax3(mc[0], x[y], x[y + 1]);
+                            mc[1] = fmax3(mc[1], x[y + 2], x[y + 3]);
+                        }
+                        mt = fmaxf(mt, fmaf(fmaxf(mc[0], mc[1]), ea[c], lg2(ev[c])));
                     }
-                    l = fmaf(r0 + r1, e[c].z, l);
+                    const bool need = mt > m + (kQtTop + kQtLazy);
+                    if (__any_sync(0xffffffffu, need)) {
+                        float c = 1.f;
+                        if (need) {
+                            c = m == -INFINITY ? 0.f : ex2(m - (mt - kQtTop));
+                            l = m == -INFINITY ? l : l * c; // 0, or NaN for good
+                            m = mt - kQtTop;
+                        }
+                        // The TMEM read-modify-write of O is warp-collective.
+                        // QK_j was issued behind PV_{j-2}, the last to write it.
+                        if (i > 1) {
+#pragma unroll 1
+                            for (int q4 = 0; q4 < DH / 16; ++q4) {
+                                uint32_t o[16];
+                                tmem_ld16_wait(t_ow + q4 * 16, o);
+#pragma unroll
+                                for (int x = 0; x < 16; ++x)
+                                    o[x] = __float_as_uint(__uint_as_float(o[x]) * c);
+                                tmem_st16(t_ow + q4 * 16, o);
+                            }
+                        }
+                    }
+                    const float nm = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                    for (int c = 0; c < NG; ++c) {
+                        constexpr int W = kTcN / NG;
+                        const float o = lg2(ev[c]) + nm;
+                        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+                        uint32_t pk[W / 2];
+#pragma unroll
+                        for (int x = 0; x < W; x += 4) {
+                            float y0, y1, y2, y3;
+                            ffma2(y0, y1, s[c * W + x], s[c * W + x + 1], ea[c], ea[c], o, o);
+                            ffma2(y2, y3, s[c * W + x + 2], s[c * W + x + 3], ea[c], ea[c], o, o);
+                            y0 = ex2(y0);
+                            y1 = ex2(y1);
+                            y2 = ex2(y2);
+                            y3 = ex2(y3);
+                            fadd2(r0, r1, r0, r1, y0, y1);
+                            fadd2(r2, r3, r2, r3, y2, y3);
+                            pk[x / 2] = pack_f16x2(y0, y1);
+                            pk[x / 2 + 1] = pack_f16x2(y2, y3);
+                            // stored 32 keys at a time (16: a group of them)
+                            if (W >= 32 && (x & 31) == 28)
+                                tmem_st16(ts + c * (W / 2) + (x & ~31) / 2, pk + (x & ~31) / 2);
+                        }
+                        if (W == 16)
+                            tmem_st8(ts + c * 8, pk);
+                        l = fmaf((r0 + r1) + (r2 + r3), 1.f / ev[c], l);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
                 }
-                // P of the tile before has been used
-                if (j >= 1 && !(ok = wait(bar_odone((j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1))))
-                    break;
-                tc_fence_after();
-                tmem_st32(t_p + wg * 32 + lane_off, pk);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar_pv(j & 1));
-            }
-            for (int i = n_own; ok && i < n; ++i) { // only the arrivals
-                const int j = j0 + i;
-                if (!(ok = wait(bar_sfull(j & 1), (uint32_t)((j >> 1) & 1))))
-                    break;
-                if (lane == 0) {
-                    mbar_arrive(bar_qk((j + 1) & 3));
-                    mbar_arrive(bar_pv(j & 1));
-                }
+                    mbar_arrive(bar_pv(wg));
             }
             if (!ok)
                 break;
             const int jl = j0 + n - 1; // last tile of the segment
+            // The warpgroup without it readies the next queries, once the last
+            // QK has finished (QK_{jl-1}, which it has seen, is behind QK_{jl-2}:
+            // the wait cannot mistake that phase).
+            if ((jl & 1) != wg &&
+                (!(ok = wait(bar_sfull(jl & 1), (uint32_t)((jl >> 1) & 1))) || !(ok = split(si + 1))))
+                break;
             s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float2(l, m);
             mbar_arrive(bar_l);
-            // The last PVs.  (The phase before on that barrier is behind QK_jl,
-            // which this warp has seen.)
+            // The last PV.  (The phase before on that barrier, PV_{jl-2}, is
+            // behind QK_jl, which every warp has seen.)
             if (!(ok = wait(bar_l, (uint32_t)(si & 1))) ||
                 !(ok = wait(bar_odone(jl & 1), (uint32_t)((jl >> 1) & 1))))
                 break;
             tc_fence_after();
-            // factors of the two O to the common maximum; O_1 is unwritten
-            // where the segment has no key in a second half
+            // factors of the two O to the common maximum; with one tile, one O
+            // is unwritten
             const float2 l0 = s_l[(si & 1) * 2 * kTcM + row], l1 = s_l[((si & 1) * 2 + 1) * kTcM + row];
-            const bool two = hi - lo > kQtStep;
+            const bool use0 = n > 1 || (j0 & 1) == 0, use1 = n > 1 || (j0 & 1) == 1;
             const float mx = fmaxf(l0.y, l1.y);
             const float f0 = l0.y == -INFINITY ? 1.f : ex2(l0.y - mx);
             const float f1 = l1.y == -INFINITY ? 1.f : ex2(l1.y - mx);
@@ -822,15 +779,15 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const size_t prow = ((size_t)blockIdx.x * 2 + sg.slot) * kTcM + row;
             constexpr int kCols = DH >= 64 ? DH / 2 : DH; // columns of O a warpgroup takes
             if (live && (DH >= 64 || wg == 0)) {
-#pragma unroll
+#pragma unroll 1
                 for (int q4 = 0; q4 < kCols / 32; ++q4) {
                     const int col = wg * kCols + q4 * 32;
                     uint32_t o[32], o1[32];
                     tmem_ld32x2_wait(t_o + lane_off + col, t_o + 128 + lane_off + col, o, o1);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float x = __uint_as_float(o[i]) * w0;
-                        o[i] = __float_as_uint(two ? fmaf(__uint_as_float(o1[i]), w1, x) : x);
+                        const float x = use0 ? __uint_as_float(o[i]) * w0 : 0.f;
+                        o[i] = __float_as_uint(use1 ? fmaf(__uint_as_float(o1[i]), w1, x) : x);
                     }
                     if (valid && sg.complete) {
                         uint4 *dst = reinterpret_cast<uint4 *>(p.pp.out + grow * DH + col);
@@ -853,7 +810,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             }
             if (valid && wg == 0)
                 (sg.complete ? p.pp.lse + grow : p.pp.part_lse + prow)[0] =
-                    ls == 0.f ? -INFINITY : ((l0.y == -INFINITY && l1.y == -INFINITY ? 0.f : mx) + __log2f(ls)) * kLn2;
+                    ls == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx) + __log2f(ls)) * kLn2;
             if (!sg.complete && sg.last_cta >= 0 && threadIdx.x == 0)
                 p.pp.cut_desc[blockIdx.x] = make_int4(nrows, sg.last_cta, sg.out_row0, 0);
             tc_fence_before();

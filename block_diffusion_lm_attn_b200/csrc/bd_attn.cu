@@ -415,14 +415,26 @@ inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T =
 // Query rows of a unit up to which the kernel for few rows takes it.
 constexpr int kQ8FewRows = 32;
 
+template <int DH, int NG>
+bd_status launch_q8_tc_ng(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
+                          int grid, cudaStream_t st)
+{
+    if (set_smem<bd::bd_decode_q8_tc_kernel<DH, NG>>(bd::kQtSmemBytes) != BD_OK)
+        return BD_ERR_CUDA;
+    bd::bd_decode_q8_tc_kernel<DH, NG><<<grid, bd::kQtThreads, bd::kQtSmemBytes, st>>>(mk, mv, p);
+    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
 template <int DH>
 bd_status launch_q8_tc(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
                        int grid, cudaStream_t st)
 {
-    if (set_smem<bd::bd_decode_q8_tc_kernel<DH>>(bd::kQtSmemBytes) != BD_OK)
-        return BD_ERR_CUDA;
-    bd::bd_decode_q8_tc_kernel<DH><<<grid, bd::kQtThreads, bd::kQtSmemBytes, st>>>(mk, mv, p);
-    return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+    switch (p.tshift) {
+    case 4: return launch_q8_tc_ng<DH, 8>(mk, mv, p, grid, st);
+    case 5: return launch_q8_tc_ng<DH, 4>(mk, mv, p, grid, st);
+    case 6: return launch_q8_tc_ng<DH, 2>(mk, mv, p, grid, st);
+    default: return launch_q8_tc_ng<DH, 1>(mk, mv, p, grid, st);
+    }
 }
 
 template <int DH, int MT>
