@@ -15,7 +15,7 @@
 //
 // Persistent, one CTA per SM, over units of a sequence, a kv-head and 128
 // query rows: whole ones, or equal ranges of 128-key tiles whose pieces
-// bd_decode_stream_combine_kernel merges (QtSource).  Roles:
+// bd_decode_q8_combine_kernel merges (QtSource).  Roles:
 //   warps 0-3, 4-7  softmax, thread = query row = TMEM lane; the warpgroups
 //                   take alternate key tiles, and the one without a segment's
 //                   last tile splits the next segment's queries meanwhile
@@ -70,6 +70,22 @@ struct QtSource {
     long long seq_base;
     int seq, seq_tiles, len, G;
 
+    // a * b / c, and a / b with the rest; 64-bit divisions, some 100 cycles
+    // each, only where the numbers ask for them
+    __device__ static long long muldiv(long long a, int b, long long c)
+    {
+        const long long x = a * b;
+        return (x | c) >> 31 ? x / c : (long long)((unsigned)x / (unsigned)c);
+    }
+    __device__ static int divmod(long long a, int b, int &rest)
+    {
+        if (a >> 31) {
+            rest = (int)(a % b);
+            return (int)(a / b);
+        }
+        rest = (int)((unsigned)a % (unsigned)b);
+        return (int)((unsigned)a / (unsigned)b);
+    }
     __device__ static int tiles_of(const PParams &p, int i, int &len)
     {
         len = i < p.B ? p.cache_len[i] : 0;
@@ -107,8 +123,8 @@ struct QtSource {
         }
         if ((int)blockIdx.x >= G)
             return;
-        t = t0 = range_start(T, G, blockIdx.x);
-        t1 = range_start(T, G, blockIdx.x + 1);
+        t = t0 = muldiv(T, blockIdx.x, G);
+        t1 = muldiv(T, blockIdx.x + 1, G);
         // the sequence that holds tile t0 < T
         for (int i0 = 0; i0 < p.B; i0 += 32) {
             const long long mine = (long long)tiles_of(p, i0 + lane, n) * ups;
@@ -138,9 +154,8 @@ struct QtSource {
             seq_base += (long long)ups * seq_tiles;
             seq_tiles = tiles_of(p, ++seq, len);
         }
-        const long long local = t - seq_base;
-        const int uis = (int)(local / seq_tiles); // unit inside the sequence
-        const int kt0 = (int)(local % seq_tiles);
+        int kt0; // first tile in the unit `uis` of the sequence
+        const int uis = divmod(t - seq_base, seq_tiles, kt0);
         const int n = (int)min((long long)(seq_tiles - kt0), t1 - t);
         const int g = uis / p.row_tiles, rt = uis % p.row_tiles;
         sg.kvhead = seq * p.Hkv + g;
@@ -157,7 +172,11 @@ struct QtSource {
         sg.slot = u0 < t0 ? 0 : 1;
         // range x starts at floor(T x / G), so the last x starting at or
         // before tile e is floor(((e + 1) G - 1) / T)
-        sg.last_cta = !sg.complete && sg.slot == 1 ? (int)(((u0 + seq_tiles) * G - 1) / T) : -1;
+        sg.last_cta = -1;
+        if (!sg.complete && sg.slot == 1) {
+            const long long e = (u0 + seq_tiles) * G - 1;
+            sg.last_cta = (e | T) >> 31 ? (int)(e / T) : (int)((unsigned)e / (unsigned)T);
+        }
         t += n;
         return true;
     }
@@ -229,6 +248,20 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t a0, uint32_t *r)
                  : "memory");
 }
 
+// two halves to two e4m3 codes, as e4m3x2
+__device__ __forceinline__ uint16_t e4m3x2_of_half2(uint32_t x)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // A query row (thread = row) as two halves of e4m3 codes, hi and lo, in the
 // 128-byte swizzle of 128-byte rows at `dst` and `dst` + kQtTile; returns the
 // row's scale.
@@ -239,19 +272,14 @@ __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint3
 #pragma unroll
     for (int i = 0; i < DH / 8; ++i)
         w[i] = valid ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
-    float amax = 0.f;
-    bool finite = true;
+    uint32_t top = 0; // non-negative bf16 order as their bits do
 #pragma unroll
     for (int i = 0; i < DH / 8; ++i) {
-        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float a = fabsf(__uint_as_float(ws[t] << 16));
-            const float b = fabsf(__uint_as_float(ws[t] & 0xffff0000u));
-            finite = finite && a < INFINITY && b < INFINITY;
-            amax = fmax3(amax, a, b);
-        }
+        top = umax_u16x2(top, umax_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+        top = umax_u16x2(top, umax_u16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
     }
+    const float amax = fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+    const bool finite = (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
     // 2^-k q reaches 448 at most; k stays where 2^k and 2^-k are normal
     const int k = max(q8_scale_exp(finite ? amax : 0.f), -100);
     const float inv = finite ? exp2_int(-k) : NAN;
@@ -265,11 +293,11 @@ __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint3
             uint32_t h[4], r[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const float a = __uint_as_float(ws[t] << 16) * inv;
-                const float b = __uint_as_float(ws[t] & 0xffff0000u) * inv;
-                h[t] = e4m3x2(a, b);
-                const float2 f = float2_of_e4m3x2((uint16_t)h[t]);
-                r[t] = e4m3x2(a - f.x, b - f.y);
+                // f16 holds 8 bits of everything that a code can show of it
+                const uint32_t x = pack_f16x2(__uint_as_float(ws[t] << 16) * inv,
+                                              __uint_as_float(ws[t] & 0xffff0000u) * inv);
+                h[t] = e4m3x2_of_half2(x);
+                r[t] = e4m3x2_of_half2(half2_sub(x, half2_of_e4m3x2((uint16_t)h[t])));
             }
             hi[2 * i] = h[0] | h[1] << 16;
             hi[2 * i + 1] = h[2] | h[3] << 16;
@@ -303,6 +331,14 @@ __device__ __forceinline__ bool qt_wait(uint32_t bar, uint32_t parity, volatile 
             return false;
         }
     }
+}
+
+// 32 bytes in one store
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // NG: scales a tile has of K and of V each, 128 / (positions per group).
@@ -789,22 +825,27 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         const float x = use0 ? __uint_as_float(o[i]) * w0 : 0.f;
                         o[i] = __float_as_uint(use1 ? fmaf(__uint_as_float(o1[i]), w1, x) : x);
                     }
-                    if (valid && sg.complete) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.pp.out + grow * DH + col);
+                    if (sg.complete) {
+                        if (valid) {
+                            bf16 *dst = p.pp.out + grow * DH + col;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint4 v4;
-                            v4.x = pack_bf16x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1]));
-                            v4.y = pack_bf16x2(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-                            v4.z = pack_bf16x2(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5]));
-                            v4.w = pack_bf16x2(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
-                            dst[i / 8] = v4;
+                            for (int i = 0; i < 32; i += 16) {
+                                uint32_t y[8];
+#pragma unroll
+                                for (int x = 0; x < 8; ++x)
+                                    y[x] = pack_bf16x2(__uint_as_float(o[i + 2 * x]), __uint_as_float(o[i + 2 * x + 1]));
+                                st_global_v8(dst + i, y);
+                            }
                         }
-                    } else if (valid) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.pp.part_o + prow * kTcD + col);
+                    } else {
+                        // column by column: 128 contiguous bytes a warp, where
+                        // 16 bytes of each of 32 rows would be as many
+                        // transactions as rows
+                        float *dst = p.pp.part_o + ((size_t)blockIdx.x * 2 + sg.slot) * (kTcM * kTcD) +
+                                     (size_t)col * kTcM + row;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            dst[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int i = 0; i < 32; ++i)
+                            dst[i * kTcM] = __uint_as_float(o[i]);
                     }
                 }
             }
@@ -829,6 +870,71 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     }
+}
+
+// Merges the pieces of the units that range boundaries cut, and fills the rows
+// of sequences without a tile, as bd_decode_stream_combine_kernel does, from
+// pieces that lie column by column ([128 columns][128 rows]): lane = row, a
+// warp takes 16 columns, so every load is one line of 128 bytes.  Grid (G, 4):
+// CTA (c, rg) takes rows 32 rg .. 32 rg + 31 of the unit of descriptor c.
+// Launched as a programmatic dependent of the attention kernel.
+template <int DH>
+__global__ void __launch_bounds__(16 * DH / 8) bd_decode_q8_combine_kernel(const PParams p)
+{
+    const int c = blockIdx.x, rg = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (rg == 0) { // an invalid length: NaN rows; mode 2 over nothing: out 0, lse -inf
+        for (int i = c; i < p.B; i += gridDim.x) {
+            const int tiles = decode_unit_tiles(p.cache_len[i], p.b, p.nkeys, p.mode);
+            if (tiles > 0)
+                continue;
+            const size_t row0 = (size_t)i * p.Hq * p.b;
+            for (long long e = threadIdx.x; e < (long long)p.Hq * p.b * DH; e += blockDim.x)
+                p.out[row0 * DH + e] = __float2bfloat16_rn(tiles < 0 ? NAN : 0.f);
+            for (int r = threadIdx.x; r < p.Hq * p.b; r += blockDim.x)
+                p.lse[row0 + r] = tiles < 0 ? NAN : -INFINITY;
+            if (threadIdx.x == 0 && tiles < 0)
+                raise_device_code(DEV_BAD_CACHE_LEN);
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 desc = p.cut_desc[c];
+    const int last = desc.y, row = rg * 32 + lane;
+    if (rg * 32 >= desc.x)
+        return;
+    float m = -INFINITY, z = 0.f, acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        acc[i] = 0.f;
+    for (int x = c; x <= last; ++x) {
+        const size_t piece = (size_t)x * 2 + (x == c ? 1 : 0);
+        const float ls = p.part_lse[piece * kTcM + row];
+        const float *src = p.part_o + piece * (kTcM * kTcD) + (size_t)warp * 16 * kTcM + row;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = src[i * kTcM];
+        if (ls == -INFINITY)
+            continue; // no visible key in this piece
+        const float mn = fmaxf(m, ls);
+        const float a = ex2((m - mn) * kLog2e); // 0 while m is -inf
+        const float w = ex2((ls - mn) * kLog2e);
+        z = z * a + w;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc[i] = acc[i] * a + w * v[i];
+        m = mn;
+    }
+    if (row >= desc.x)
+        return;
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        y[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    st_global_v8(p.out + ((size_t)desc.z + row) * DH + warp * 16, y);
+    if (warp == 0)
+        p.lse[(size_t)desc.z + row] = z == 0.f ? -INFINITY : m + __logf(z);
 }
 
 } // namespace bd

@@ -341,25 +341,32 @@ bd_status decode_validate(const void *q_blk, const void *k_cache,
     return BD_OK;
 }
 
-// Programmatic dependent launch of the merge of cut units: its blocks may be
+// Programmatic dependent launch of a merge of cut units: its blocks may be
 // placed while the attention kernel before it runs; they wait for its end
 // in-kernel.
-template <bool KEEP_NAN>
-bd_status launch_combine(const bd::PParams &p, int G, cudaStream_t stream)
+bd_status launch_dependent(void (*kernel)(const bd::PParams), dim3 grid, int threads,
+                           const bd::PParams &p, cudaStream_t stream)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(G, bd::kCombineRowGroups);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = 0;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, bd::bd_decode_stream_combine_kernel<KEEP_NAN>, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess)
         return BD_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
+template <bool KEEP_NAN>
+bd_status launch_combine(const bd::PParams &p, int G, cudaStream_t stream)
+{
+    return launch_dependent(bd::bd_decode_stream_combine_kernel<KEEP_NAN>,
+                            dim3(G, bd::kCombineRowGroups), 256, p, stream);
 }
 
 // Launches block decode with a validated plan and a workspace of at least
@@ -448,7 +455,8 @@ bd_status launch_q8_rows(const CUtensorMap &mk, const CUtensorMap &mv, const bd:
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 
-// The 8-bit decode's attention kernel for these rows per unit.
+// The 8-bit decode: the attention kernel for these rows per unit, and the merge
+// of its cut units.
 template <int DH>
 bd_status launch_q8(const void *k_cache, const void *v_cache, const bd::QtParams &p, int grid,
                     cudaStream_t st)
@@ -460,10 +468,15 @@ bd_status launch_q8(const void *k_cache, const void *v_cache, const bd::QtParams
     if (!make_map_codes(&mk, k_cache, (uint64_t)p.pp.nkeys, heads, DH, cols, keys) ||
         !make_map_codes(&mv, v_cache, (uint64_t)p.pp.nkeys, heads, DH, cols, keys))
         return BD_ERR_CUDA;
-    if (!rows)
-        return launch_q8_tc<DH>(mk, mv, p, grid, st);
-    return p.pp.rows_unit <= 16 ? launch_q8_rows<DH, 1>(mk, mv, p, grid, st)
-                                : launch_q8_rows<DH, 2>(mk, mv, p, grid, st);
+    if (!rows) {
+        const bd_status r = launch_q8_tc<DH>(mk, mv, p, grid, st);
+        return r != BD_OK ? r
+                          : launch_dependent(bd::bd_decode_q8_combine_kernel<DH>, dim3(grid, 4),
+                                             16 * DH / 8, p.pp, st);
+    }
+    const bd_status r = p.pp.rows_unit <= 16 ? launch_q8_rows<DH, 1>(mk, mv, p, grid, st)
+                                             : launch_q8_rows<DH, 2>(mk, mv, p, grid, st);
+    return r != BD_OK ? r : launch_combine<true>(p.pp, grid, st);
 }
 
 // Host-side checks shared by the calls on a cache in 8 bits.
@@ -1002,10 +1015,9 @@ bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache, const void *
     p.groups = (int)cdiv(S_cap, group);
     p.tshift = group == 16 ? 4 : group == 32 ? 5 : group == 64 ? 6 : 7;
     const int G = persistent_grid();
-    st = d == 128  ? launch_q8<128>(k_cache, v_cache, p, G, stream)
-         : d == 64 ? launch_q8<64>(k_cache, v_cache, p, G, stream)
-                   : launch_q8<32>(k_cache, v_cache, p, G, stream);
-    return st == BD_OK ? launch_combine<true>(p.pp, G, stream) : st;
+    return d == 128  ? launch_q8<128>(k_cache, v_cache, p, G, stream)
+           : d == 64 ? launch_q8<64>(k_cache, v_cache, p, G, stream)
+                     : launch_q8<32>(k_cache, v_cache, p, G, stream);
 }
 
 bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
