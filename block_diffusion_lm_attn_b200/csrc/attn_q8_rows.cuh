@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kQrThreads, 1)
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    QtSource src;
+    QtSource<5> src;
     src.init(p.pp);
     Seg sg, nx;
     bool more = src.next(p.pp, nx);

@@ -59,14 +59,18 @@ constexpr int kQtSmemBytes = kQtSmemBar + 512 + 1024; // + alignment slack
 static_assert(kQtSmemBytes <= 227 * 1024, "more shared memory than a CTA may have");
 
 // The work list, walked by one converged warp.  It is DecSource's (units x
-// tiles, cut into equal ranges, or whole units) but for three things: the
-// warp reads 32 lengths at a time (one after another they took 3 us for 16
-// sequences and 8 us for 64, at the head of every launch); no more CTAs take
+// tiles, cut into equal ranges, or whole units) but for four things.  The warp
+// reads 32 lengths at a time (one after another they took 3 us for 16
+// sequences and 8 us for 64, at the head of every launch).  No more CTAs take
 // part than there are tiles, so that the merge of a short launch walks over no
-// empty pieces; and units stay whole only where the longest is at most 3 tiles
-// above the mean of the CTAs, about what merging costs.
+// empty pieces.  Units stay whole only where the longest is at most 3 tiles
+// above the mean of the CTAs, about what merging costs.  And a range is not so
+// many tiles, but so much work: in front of each unit's tiles lie kHead
+// positions for what a segment costs besides its tiles.
+template <int HEAD>
 struct QtSource {
-    long long t, t1, t0, T;
+    static constexpr int kHead = HEAD;
+    long long t, t1, t0, T; // positions: next, end and start of this CTA's, all
     long long seq_base;
     int seq, seq_tiles, len, G;
 
@@ -91,33 +95,44 @@ struct QtSource {
         len = i < p.B ? p.cache_len[i] : 0;
         return i < p.B ? max(0, decode_unit_tiles(len, p.b, p.nkeys, p.mode)) : 0;
     }
+    // positions of a unit of so many tiles
+    __device__ static int span(int tiles) { return tiles ? tiles + kHead : 0; }
     __device__ void init(const PParams &p)
     {
         const int lane = threadIdx.x & 31;
         const int ups = p.Hkv * p.row_tiles; // units per sequence
-        long long sum = 0;
-        int maxt = 0, n;
+        long long sum = 0, sum_pos = 0;
+        int maxt = 0, n, first = 0; // tiles of sequence `lane`
         for (int i = lane; i < p.B; i += 32) {
             const int ti = tiles_of(p, i, n);
+            first = i == lane ? ti : first;
             sum += ti;
+            sum_pos += span(ti);
             maxt = max(maxt, ti);
         }
+        if (p.B <= 32) { // tiles of a sequence are below 2^23
+            sum = __reduce_add_sync(0xffffffffu, (unsigned)sum);
+            sum_pos = __reduce_add_sync(0xffffffffu, (unsigned)sum_pos);
+        } else {
 #pragma unroll
-        for (int o = 16; o; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            for (int o = 16; o; o >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                sum_pos += __shfl_xor_sync(0xffffffffu, sum_pos, o);
+            }
+        }
         maxt = __reduce_max_sync(0xffffffffu, maxt);
-        T = sum * ups;
-        G = (int)min((long long)gridDim.x, max(T, 1LL));
-        const long long units = (long long)p.B * ups;
+        const long long tiles = sum * ups, units = (long long)p.B * ups;
+        T = sum_pos * ups;
+        G = (int)min((long long)gridDim.x, max(tiles, 1LL));
         t = t0 = t1 = seq_base = 0;
         seq = seq_tiles = len = 0;
-        if (units <= gridDim.x && (long long)(maxt - 3) * G <= T) {
+        if (units <= gridDim.x && (long long)(maxt - 3) * G <= tiles) {
             // CTA c takes unit c
             if (blockIdx.x < units) {
                 seq = blockIdx.x / ups;
                 seq_tiles = tiles_of(p, seq, len);
-                t = t0 = (long long)(blockIdx.x % ups) * seq_tiles;
-                t1 = t0 + seq_tiles;
+                t = t0 = (long long)(blockIdx.x % ups) * span(seq_tiles);
+                t1 = t0 + span(seq_tiles);
             }
             return;
         }
@@ -125,9 +140,9 @@ struct QtSource {
             return;
         t = t0 = muldiv(T, blockIdx.x, G);
         t1 = muldiv(T, blockIdx.x + 1, G);
-        // the sequence that holds tile t0 < T
+        // the sequence that holds position t0 < T
         for (int i0 = 0; i0 < p.B; i0 += 32) {
-            const long long mine = (long long)tiles_of(p, i0 + lane, n) * ups;
+            const long long mine = (long long)span(i0 ? tiles_of(p, i0 + lane, n) : first) * ups;
             long long incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -147,38 +162,43 @@ struct QtSource {
     }
     __device__ bool next(const PParams &p, Seg &sg)
     {
-        if (t >= t1)
-            return false;
         const int ups = p.Hkv * p.row_tiles;
-        while (t >= seq_base + (long long)ups * seq_tiles) {
-            seq_base += (long long)ups * seq_tiles;
-            seq_tiles = tiles_of(p, ++seq, len);
+        for (;;) {
+            if (t >= t1)
+                return false;
+            while (t >= seq_base + (long long)ups * span(seq_tiles)) {
+                seq_base += (long long)ups * span(seq_tiles);
+                seq_tiles = tiles_of(p, ++seq, len);
+            }
+            int at; // position in the unit `uis` of the sequence
+            const int uis = divmod(t - seq_base, span(seq_tiles), at);
+            const int kt0 = max(at - kHead, 0);
+            const int n = (int)min((long long)(span(seq_tiles) - at), t1 - t) - (kt0 - at + kHead);
+            const long long u0 = t - at + kHead; // position of the unit's first tile
+            t = t - at + kHead + kt0 + max(n, 0);
+            if (n <= 0) // the range ends in front of the unit's first tile
+                return false;
+            const int g = uis / p.row_tiles, rt = uis % p.row_tiles;
+            sg.kvhead = seq * p.Hkv + g;
+            sg.qrow0 = rt * kTcM;
+            sg.nrows = min(kTcM, p.rows_unit - rt * kTcM);
+            sg.lo0 = kt0 * kTcN;
+            sg.hi0 = min((kt0 + n) * kTcN, len + decode_own_keys(p.b, p.mode));
+            sg.fhi0 = len + (p.mode == 0 ? p.b : 0);
+            sg.nt = n;
+            sg.len = len;
+            sg.out_row0 = (seq * p.Hq + g * (p.Hq / p.Hkv)) * p.b + rt * kTcM;
+            sg.complete = n == seq_tiles;
+            sg.slot = u0 < t0 ? 0 : 1;
+            // range x starts at floor(T x / G), so the last x starting at or
+            // before position e is floor(((e + 1) G - 1) / T)
+            sg.last_cta = -1;
+            if (!sg.complete && sg.slot == 1) {
+                const long long e = (u0 + seq_tiles) * G - 1;
+                sg.last_cta = (e | T) >> 31 ? (int)(e / T) : (int)((unsigned)e / (unsigned)T);
+            }
+            return true;
         }
-        int kt0; // first tile in the unit `uis` of the sequence
-        const int uis = divmod(t - seq_base, seq_tiles, kt0);
-        const int n = (int)min((long long)(seq_tiles - kt0), t1 - t);
-        const int g = uis / p.row_tiles, rt = uis % p.row_tiles;
-        sg.kvhead = seq * p.Hkv + g;
-        sg.qrow0 = rt * kTcM;
-        sg.nrows = min(kTcM, p.rows_unit - rt * kTcM);
-        sg.lo0 = kt0 * kTcN;
-        sg.hi0 = min((kt0 + n) * kTcN, len + decode_own_keys(p.b, p.mode));
-        sg.fhi0 = len + (p.mode == 0 ? p.b : 0);
-        sg.nt = n;
-        sg.len = len;
-        sg.out_row0 = (seq * p.Hq + g * (p.Hq / p.Hkv)) * p.b + rt * kTcM;
-        sg.complete = n == seq_tiles;
-        const long long u0 = seq_base + (long long)uis * seq_tiles;
-        sg.slot = u0 < t0 ? 0 : 1;
-        // range x starts at floor(T x / G), so the last x starting at or
-        // before tile e is floor(((e + 1) G - 1) / T)
-        sg.last_cta = -1;
-        if (!sg.complete && sg.slot == 1) {
-            const long long e = (u0 + seq_tiles) * G - 1;
-            sg.last_cta = (e | T) >> 31 ? (int)(e / T) : (int)((unsigned)e / (unsigned)T);
-        }
-        t += n;
-        return true;
     }
 };
 
@@ -226,7 +246,7 @@ __device__ __forceinline__ float lg2(float x)
 // P reaches 2^kQtTop where the maximum was last raised, and 2^(kQtTop +
 // kQtLazy) before it is raised again: the largest f16 is above 2^15, and the
 // smallest normal one then 2^-20 of the row's largest P.
-constexpr float kQtTop = 6.f, kQtLazy = 8.f;
+constexpr float kQtTop = 3.f, kQtLazy = 12.f;
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
 {
@@ -400,6 +420,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    if (warp == 8 && lane < 2) // the first copy would wait for its map
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tm_v : &tm_k)) : "memory");
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32((const void *)tmem_slot)), "r"(512));
@@ -419,7 +441,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 
     if (warp == 8) {
         // -------------------------- work list; loads of K, V and the scales
-        QtSource src;
+        QtSource<5> src;
         src.init(p.pp);
         if (lane == 0)
             p.pp.cut_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -443,6 +465,12 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             __syncwarp();
             if (!got)
                 break;
+            // its queries, which a warpgroup reads when the segment before is
+            // all but done
+            if (si > 0)
+                for (int e = lane * 128; e < sg.nrows * DH * 2; e += 32 * 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        reinterpret_cast<const char *>(p.q + (size_t)sg.out_row0 * DH) + e));
             for (int it = 0; it < sg.nt; ++it, ++g) {
                 const int ks = sg.lo0 + it * kTcN, s = g & 3;
                 if (g >= 4 && !(ok = wait(bar_kempty(s), (uint32_t)((g >> 2) & 1) ^ 1u)))
