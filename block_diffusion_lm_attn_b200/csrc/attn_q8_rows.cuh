@@ -1,17 +1,20 @@
 // Block decode over a KV cache in 8 bits for few query rows (sm_100a).
 //
 // The mathematics of attn_q8_tc.cuh, for units (a sequence and a kv-head) of
-// at most 32 query rows, single tokens above all.  There the 128-row tile of
-// tcgen05 would be almost empty while its softmax still walks 128 columns a
-// tile; here a warp takes 16 x MT rows with mma.sync.m16n8k16, and what a key
-// costs is fetching and converting its 2 d codes.
+// at most 16 query rows (32 at d = 32), single tokens above all.  There the
+// 128-row tile of tcgen05 would be almost empty while its softmax still walks 128
+// columns a tile; here a warp takes 16 x MT rows with mma.sync.m16n8k16, and what
+// a key costs is fetching and converting its 2 d codes.
 //
 // Bound by HBM, then by the instructions of a key (about 15 a warp, two thirds
 // of them the conversion of codes to f16).  So: one persistent CTA per SM, 8
 // warps, each on its own: its own ring of two 8 KB stages of K and V filled by
 // TMA, its own running maximum, sum and O in registers, no barrier between
 // warps until the segment's end, where the 8 results meet in shared memory.
-// Segments are QtSource's, cut units are merged by the same second kernel.
+// Segments are QtSource's; cut units are merged by bd_decode_stream_combine_kernel.
+// Measured: single tokens of 24 prefixes of 4096 to 32768 keys, 32 query heads on
+// 8, d = 128: 148 us, 5.6 TB/s (165 us, 5.1 TB/s, where calls in a row hold the
+// card at its power limit); on the 128-row tiles 268 us at the time.
 //
 // Operands straight from the codes as they lie: the order of d within a
 // product, and of the columns of O, is free as long as both sides share it.

@@ -419,8 +419,12 @@ inline bool aligned4(const void *p)
 // Group sizes of a cache in 8 bits: whole 16-key chunks of a key tile.
 inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
 
-// Query rows of a unit up to which the kernel for few rows takes it.
-constexpr int kQ8FewRows = 32;
+// Query rows of a unit up to which the kernel for few rows takes it: 16 at a
+// time, and at d = 32 twice 16.  Measured over 24 prefixes of 4096 to 32768 keys,
+// 8 kv-heads: 16 rows 156 us here, 187 us on the 128-row tiles (d = 128); 17 to 32
+// rows 129 us and 158 us at d = 32, 161 us and 162 us at d = 64, 284 us (registers
+// spill) and 190 us at d = 128.
+constexpr int q8_few_rows(int d) { return d == 32 ? 32 : 16; }
 
 template <int DH, int NG>
 bd_status launch_q8_tc_ng(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
@@ -461,7 +465,7 @@ template <int DH>
 bd_status launch_q8(const void *k_cache, const void *v_cache, const bd::QtParams &p, int grid,
                     cudaStream_t st)
 {
-    const bool rows = p.pp.rows_unit <= kQ8FewRows;
+    const bool rows = p.pp.rows_unit <= q8_few_rows(DH);
     const uint32_t cols = rows ? DH : 128, keys = rows ? bd::kQrTile / DH : 128;
     CUtensorMap mk, mv;
     const uint64_t heads = (uint64_t)p.pp.B * p.pp.Hkv;
@@ -474,8 +478,13 @@ bd_status launch_q8(const void *k_cache, const void *v_cache, const bd::QtParams
                           : launch_dependent(bd::bd_decode_q8_combine_kernel<DH>, dim3(grid, 4),
                                              16 * DH / 8, p.pp, st);
     }
-    const bd_status r = p.pp.rows_unit <= 16 ? launch_q8_rows<DH, 1>(mk, mv, p, grid, st)
-                                             : launch_q8_rows<DH, 2>(mk, mv, p, grid, st);
+    bd_status r;
+    if constexpr (q8_few_rows(DH) > 16) {
+        r = p.pp.rows_unit <= 16 ? launch_q8_rows<DH, 1>(mk, mv, p, grid, st)
+                                 : launch_q8_rows<DH, 2>(mk, mv, p, grid, st);
+    } else {
+        r = launch_q8_rows<DH, 1>(mk, mv, p, grid, st);
+    }
     return r != BD_OK ? r : launch_combine<true>(p.pp, grid, st);
 }
 
