@@ -353,14 +353,6 @@ __device__ __forceinline__ bool qt_wait(uint32_t bar, uint32_t parity, volatile 
     }
 }
 
-// 32 bytes in one store
-__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 // NG: scales a tile has of K and of V each, 128 / (positions per group).
 template <int DH, int NG>
 __global__ void __launch_bounds__(kQtThreads, 1)
@@ -862,7 +854,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 #pragma unroll
                                 for (int x = 0; x < 8; ++x)
                                     y[x] = pack_bf16x2(__uint_as_float(o[i + 2 * x]), __uint_as_float(o[i + 2 * x + 1]));
-                                st_global_v8(dst + i, y);
+                                st32(dst + i, y);
                             }
                         }
                     } else {
@@ -960,7 +952,7 @@ __global__ void __launch_bounds__(16 * DH / 8) bd_decode_q8_combine_kernel(const
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         y[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    st_global_v8(p.out + ((size_t)desc.z + row) * DH + warp * 16, y);
+    st32(p.out + ((size_t)desc.z + row) * DH + warp * 16, y);
     if (warp == 0)
         p.lse[(size_t)desc.z + row] = z == 0.f ? -INFINITY : m + __logf(z);
 }

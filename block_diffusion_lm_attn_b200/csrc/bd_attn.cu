@@ -933,13 +933,12 @@ bd_status bd_cache_append_q8(void *k_cache, void *v_cache, float *k_scale,
         // the first group may hold older rows: one group more than b rows fill
         const unsigned touched = (unsigned)std::min<long long>(cdiv(b, group) + 1, p.groups);
         const dim3 grid(touched, 2 * Hkv, B);
-        const int vec = group * d / 8;
+        const int vec = group * d / 16;
         const int threads = std::min(bd::kQ8Threads, vec);
         switch ((vec + threads - 1) / threads) {
         case 1: bd::bd_cache_append_q8_kernel<1><<<grid, threads, 0, stream>>>(p); break;
         case 2: bd::bd_cache_append_q8_kernel<2><<<grid, threads, 0, stream>>>(p); break;
-        case 4: bd::bd_cache_append_q8_kernel<4><<<grid, threads, 0, stream>>>(p); break;
-        default: bd::bd_cache_append_q8_kernel<8><<<grid, threads, 0, stream>>>(p); break;
+        default: bd::bd_cache_append_q8_kernel<4><<<grid, threads, 0, stream>>>(p); break;
         }
         if (cudaGetLastError() != cudaSuccess)
             return BD_ERR_CUDA;

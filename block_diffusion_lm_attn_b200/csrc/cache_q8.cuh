@@ -13,7 +13,10 @@
 //
 // Bound by HBM: 2 bytes read and 1 written per value on the way in, the
 // reverse on the way back; the rows that share the first written group are
-// read once more.
+// read once more.  Measured: a prompt of 8192 rows (4 sequences, 8 kv-heads, d =
+// 128) into an empty cache 31.7 us, 6.4 TB/s (with half the values a thread and
+// accesses of 16 and 8 bytes 37.7, with floats in registers 99); up to 28 rows
+// behind 64 prefixes 7.6 us; 16 sequences of 4001 to 8192 rows back 94 us, 6.5 TB/s.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -35,6 +38,35 @@ struct Q8Params {
     bf16 *k_out, *v_out;        // read back: [B, Hkv, S_cap, d]
     int B, Hkv, b, d, S_cap, T, groups;
 };
+
+// 32 bytes at a 16-byte aligned address, in one access where it is a multiple of
+// 32 (a warp's lanes then cover whole lines at once: reading a cache back took 103
+// us with two stores of 16 bytes a lane and takes 94 us)
+__device__ __forceinline__ void st32(void *p, const uint32_t *r)
+{
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else {
+        uint4 *q = static_cast<uint4 *>(p);
+        q[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        q[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+}
+__device__ __forceinline__ void ld32(const void *p, uint32_t *r)
+{
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = static_cast<const uint4 *>(p)[0], b = static_cast<const uint4 *>(p)[1];
+        r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+        r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+    }
+}
 
 // two floats to two e4m3 codes, lo in the low byte: round to nearest even,
 // +-448 beyond the range, NaN kept
@@ -79,9 +111,9 @@ __device__ __forceinline__ uint32_t umax_u16x2(uint32_t a, uint32_t b)
 }
 
 // One CTA per (touched group, kv-head and K or V, sequence).  NV: vectors of
-// 8 values a thread, held in registers between the maximum and the codes as
-// they were read (bf16, or codes of rows that stay): 4 registers a vector
-// where floats took 8, and so four CTAs to an SM where there were two.
+// 16 values a thread, held in registers between the maximum and the codes as
+// they were read (bf16, or codes of rows that stay): 8 registers a vector
+// where floats took 16, and so four CTAs to an SM where there were two.
 // Non-negative bf16 order as their bits do, so the maximum is taken on pairs
 // of 16 bits.
 template <int NV>
@@ -104,58 +136,63 @@ __global__ void __launch_bounds__(kQ8Threads, 4)
     uint8_t *codes = (is_v ? p.v_cache : p.k_cache) + head * p.S_cap * p.d;
     float *scale = (is_v ? p.v_scale : p.k_scale) + head * p.groups + g;
     const bf16 *src = (is_v ? p.v_new : p.k_new) + head * p.b * p.d;
-    const int vpr = p.d / 8; // vectors per row: a power of two
+    const int vpr = p.d / 16; // vectors per row: a power of two
     const int shift = 31 - __clz(vpr);
     const int total = p.T * vpr;
     const float old = *scale;
     const int row0 = g * p.T;
 
-    uint4 w[NV];
+    uint32_t w[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int e = v * blockDim.x + threadIdx.x;
-        const int row = row0 + (e >> shift), col = (e & (vpr - 1)) * 8;
-        w[v] = make_uint4(0, 0, 0, 0);
+        const int row = row0 + (e >> shift), col = (e & (vpr - 1)) * 16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            w[v][k] = 0;
         if (e < total && row >= len && row < len + n) {
-            w[v] = *reinterpret_cast<const uint4 *>(src + (size_t)(row - len) * p.d + col);
+            ld32(src + (size_t)(row - len) * p.d + col, w[v]);
         } else if (e < total && row < len) {
-            const uint2 c = *reinterpret_cast<const uint2 *>(codes + (size_t)row * p.d + col);
-            w[v].x = c.x;
-            w[v].y = c.y;
+            const uint4 c = *reinterpret_cast<const uint4 *>(codes + (size_t)row * p.d + col);
+            w[v][0] = c.x; w[v][1] = c.y; w[v][2] = c.z; w[v][3] = c.w;
         }
     }
-    // the 8 values of vector v
-    auto values = [&](int v, bool kept, float *x) {
-        const uint32_t ws[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+    // values 8 k .. 8 k + 7 of vector v
+    auto values = [&](int v, int k, bool kept, float *x) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if (kept) {
-                const float2 f = float2_of_e4m3x2((uint16_t)(ws[t >> 1] >> (16 * (t & 1))));
+                const float2 f = float2_of_e4m3x2((uint16_t)(w[v][2 * k + (t >> 1)] >> (16 * (t & 1))));
                 x[2 * t] = f.x * old;
                 x[2 * t + 1] = f.y * old;
             } else {
-                x[2 * t] = __uint_as_float(ws[t] << 16);
-                x[2 * t + 1] = __uint_as_float(ws[t] & 0xffff0000u);
+                x[2 * t] = __uint_as_float(w[v][4 * k + t] << 16);
+                x[2 * t + 1] = __uint_as_float(w[v][4 * k + t] & 0xffff0000u);
             }
         }
     };
     float amax = 0.f; // of the finite values
-    uint32_t top = 0;
+    auto finite_max = [&](int v, bool kept) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        if (row0 + ((v * (int)blockDim.x + (int)threadIdx.x) >> shift) < len) {
+        for (int k = 0; k < 2; ++k) {
             float x[8];
-            values(v, true, x);
+            values(v, k, kept, x);
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 const float m = fabsf(x[t]);
                 amax = m < INFINITY ? fmaxf(amax, m) : amax;
             }
+        }
+    };
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        if (row0 + ((v * (int)blockDim.x + (int)threadIdx.x) >> shift) < len) {
+            finite_max(v, true);
         } else {
-            top = umax_u16x2(top, w[v].x & 0x7fff7fffu);
-            top = umax_u16x2(top, w[v].y & 0x7fff7fffu);
-            top = umax_u16x2(top, w[v].z & 0x7fff7fffu);
-            top = umax_u16x2(top, w[v].w & 0x7fff7fffu);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                top = umax_u16x2(top, w[v][k] & 0x7fff7fffu);
         }
     }
     if ((top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u) {
@@ -164,13 +201,7 @@ __global__ void __launch_bounds__(kQ8Threads, 4)
         for (int v = 0; v < NV; ++v) {
             if (row0 + ((v * (int)blockDim.x + (int)threadIdx.x) >> shift) < len)
                 continue;
-            float x[8];
-            values(v, false, x);
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const float m = fabsf(x[t]);
-                amax = m < INFINITY ? fmaxf(amax, m) : amax;
-            }
+            finite_max(v, false);
         }
     }
     amax = fmaxf(amax, fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u)));
@@ -187,21 +218,24 @@ __global__ void __launch_bounds__(kQ8Threads, 4)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int e = v * blockDim.x + threadIdx.x;
-        const int row = row0 + (e >> shift), col = (e & (vpr - 1)) * 8;
+        const int row = row0 + (e >> shift), col = (e & (vpr - 1)) * 16;
         // rows that stay keep their codes under the same scale
         if (e >= total || row >= len + n || (row < len && s == old))
             continue;
-        float x[8];
-        if (row < len)
-            values(v, true, x);
-        else
-            values(v, false, x);
-        uint2 c;
-        c.x = (uint32_t)e4m3x2(x[0] * inv, x[1] * inv) |
-              (uint32_t)e4m3x2(x[2] * inv, x[3] * inv) << 16;
-        c.y = (uint32_t)e4m3x2(x[4] * inv, x[5] * inv) |
-              (uint32_t)e4m3x2(x[6] * inv, x[7] * inv) << 16;
-        *reinterpret_cast<uint2 *>(codes + (size_t)row * p.d + col) = c;
+        uint32_t c[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float x[8];
+            if (row < len)
+                values(v, k, true, x);
+            else
+                values(v, k, false, x);
+            c[2 * k] = (uint32_t)e4m3x2(x[0] * inv, x[1] * inv) |
+                       (uint32_t)e4m3x2(x[2] * inv, x[3] * inv) << 16;
+            c[2 * k + 1] = (uint32_t)e4m3x2(x[4] * inv, x[5] * inv) |
+                           (uint32_t)e4m3x2(x[6] * inv, x[7] * inv) << 16;
+        }
+        *reinterpret_cast<uint4 *>(codes + (size_t)row * p.d + col) = make_uint4(c[0], c[1], c[2], c[3]);
     }
     if (threadIdx.x == 0)
         *scale = s;
@@ -226,8 +260,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // Rows 0 .. cache_len[i]-1 back to bf16 (exact for a power-of-two scale, else
-// rounded to nearest even).  A thread takes 16 codes; grid: x = runs of
-// 16-code vectors of one head, y = kv-head and K or V, z = sequence.
+// rounded to nearest even).  A thread takes 16 codes and writes 32 bytes at
+// once; grid: x = runs of 16-code vectors of one head, y = kv-head and K or V, z =
+// sequence.  (Two and four vectors a thread, all loads first: 1 and 8 % slower.)
 __global__ void __launch_bounds__(kQ8Threads)
     bd_cache_read_q8_kernel(const Q8Params p)
 {
@@ -240,11 +275,11 @@ __global__ void __launch_bounds__(kQ8Threads)
     }
     const size_t head = (size_t)i * p.Hkv + h;
     const long long e = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 16;
-    const int row = (int)(e / p.d);
-    if (row >= len)
+    if (e >= (long long)len * p.d)
         return;
     const uint8_t *codes = (is_v ? p.v_cache : p.k_cache) + head * p.S_cap * p.d;
-    const float s = (is_v ? p.v_scale : p.k_scale)[head * p.groups + row / p.T];
+    const int shift = 31 - __clz(p.d * p.T); // codes of a group: a power of two
+    const float s = (is_v ? p.v_scale : p.k_scale)[head * p.groups + (e >> shift)];
     bf16 *out = (is_v ? p.v_out : p.k_out) + head * p.S_cap * p.d;
     const uint4 w = *reinterpret_cast<const uint4 *>(codes + e);
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -254,9 +289,7 @@ __global__ void __launch_bounds__(kQ8Threads)
         const float2 f = float2_of_e4m3x2((uint16_t)(ws[t >> 1] >> (16 * (t & 1))));
         o[t] = pack_bf16x2(f.x * s, f.y * s);
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(out + e);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    st32(out + e, o);
 }
 
 } // namespace bd

@@ -15,14 +15,16 @@
 // few sequences by latency: the gathers of the acceptance, the rows, the entry
 // in its segment, each waits for the one before.  A cluster of 8 CTAs takes a
 // sequence, an eighth of the vocabulary each, and exchanges the eight sums
-// through shared memory; a lane has 32 loads in flight.  Measured: 7.8 us for
-// one sequence of 50001 entries (one CTA a sequence: 36), 15.7 us for 64 of
-// 131072 (137; 16 loads in flight: 29), 4.3 TB/s.
+// through shared memory; a lane has 32 numbers on their way.  Measured: 7.5 us
+// for one sequence of 50001 entries (one CTA a sequence: 36), 19.3 us for 64 of
+// 131072, 3.5 TB/s (137; half as many numbers on their way: 29; rows that are not
+// on 32-byte boundaries: 20.8).
 #pragma once
 
 #include <limits.h>
 
 #include "bd_common.cuh"
+#include "cache_q8.cuh"
 
 namespace bd {
 
@@ -174,14 +176,40 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(THREADS
             use(e, a[e] > b[e] ? (double)a[e] - (double)b[e] : 0.0);
         }
     };
+    // rows on 32-byte boundaries: weights of entries t .. t + 7 and 256 on, 8 at
+    // a load
+    const bool wide = ((reinterpret_cast<uintptr_t>(pr) | reinterpret_cast<uintptr_t>(qr)) & 31) == 0;
+    auto wide_weights = [&](int t, auto use) {
+        static_assert(E == 16, "two runs of 8");
+        uint32_t a[16], b[16];
+        ld32(pr + t, a);
+        ld32(pr + t + 256, a + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            b[e] = 0;
+        if (residual && qr) {
+            ld32(qr + t, b);
+            ld32(qr + t + 256, b + 8);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float x = __uint_as_float(a[e]);
+            const float y = residual && t + (e & 7) + 32 * (e & 8) == point ? 1.f : __uint_as_float(b[e]);
+            use(e, x > y ? (double)x - (double)y : 0.0);
+        }
+    };
     double total = 0.0, before = 0.0; // of the cluster; of the CTAs before this one
     int owner_last = -1;              // last CTA with mass
     int pass = 0;
     for (;; ++pass) {
         for (int g = warp; g < mine; g += THREADS / 32) {
             double part = 0.0;
-            weights(v0 + g * kVerifySeg + lane, 32, v0 + (g + 1) * kVerifySeg <= v1,
-                    [&](int, double w) { part += w; });
+            const int t0 = v0 + g * kVerifySeg;
+            auto add = [&](int, double w) { part += w; };
+            if (wide && t0 + kVerifySeg <= v1)
+                wide_weights(t0 + 8 * lane, add);
+            else
+                weights(t0 + lane, 32, t0 + kVerifySeg <= v1, add);
             part = warp_sum(part);
             if (lane == 0)
                 seg[g] = part;

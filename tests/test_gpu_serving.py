@@ -471,6 +471,47 @@ def test_decode_is_deterministic_and_takes_a_workspace_and_a_stream():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def off16(shape, dtype=torch.bfloat16):
+    """A contiguous buffer on a 16-byte boundary that is none of 32 bytes."""
+    n = math.prod(shape)
+    t = torch.zeros(n + 16, dtype=dtype, device="cuda")[8:8 + n].view(shape)
+    assert t.data_ptr() % 32 == 16 and t.is_contiguous()
+    return t
+
+
+@pytest.mark.parametrize("b", [1, 40])
+def test_buffers_on_16_byte_boundaries(b):
+    """New rows, read-back rows, queries and outputs where a 32-byte access
+    would be misaligned; whole units and cut ones."""
+    lens = [600, 40]
+    q, kv = decode_case(2, 4, 2, b, 128, 700, 32, lens, 0, 87)
+    (kc, ks), (vc, vs) = kv
+    k, v = (serving.values(c.numpy(), s.numpy(), 32) for c, s in kv)
+    for grid in (0, 3):
+        assert bd.bd_attn_debug_set_grid(grid) == bd.BD_OK
+        try:
+            qd, out = off16(q.shape), off16(q.shape)
+            qd.copy_(q)
+            _, lse = bd.decode_q8(qd, cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 0, 32, out=out)
+            ok()
+            check_decode(out, lse, q, k, v, lens, 0)
+        finally:
+            bd.bd_attn_debug_set_grid(0)
+    ko, vo = off16(k.shape), off16(k.shape)
+    bd.cache_read_q8(cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 32, k_out=ko, v_out=vo)
+    new = off16((2, 2, b, 128))
+    new.copy_(randn(gen(88), 2, 2, b, 128))
+    dev = [cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda()]
+    bd.cache_append_q8(*dev, i32(lens).cuda(), new, new, 32)
+    ok()
+    for i, n in enumerate(lens):
+        np.testing.assert_array_equal(f64(ko)[i, :, :n], k[i, :, :n])
+        np.testing.assert_array_equal(f64(vo)[i, :, :n], v[i, :, :n])
+    rc, rs = serving.append_q8(kc.numpy(), ks.numpy(), lens, f64(new), [b, b], 32)
+    for i, n in enumerate(lens):
+        np.testing.assert_array_equal(bits(dev[0])[i, :, :n + b], rc[i, :, :n + b])
+
+
 # ----------------------------------------------------------------------------
 # verification
 
@@ -496,7 +537,7 @@ def run_verify(x, q, p, u, r, nd):
         assert (int(n[i]), int(t[i])) == want, i
 
 
-@pytest.mark.parametrize("V", [1, 2, 31, 1000, 1024, 1025, 50001])
+@pytest.mark.parametrize("V", [1, 2, 31, 1000, 1024, 1025, 8192, 50001])
 @pytest.mark.parametrize("point", [False, True])
 def test_verify_matches_the_definition(V, point):
     run_verify(*verify_case(9, 5, V, V, point))
