@@ -28,12 +28,19 @@
 //
 // Each warpgroup has an O, a running maximum and a sum of its own, joined in
 // the epilogue, so that a tile costs a softmax warp one wait (for S) and one
-// arrival (of P).  That count is what bounds the kernel: between two waits a
-// warp issues an instruction every 5 cycles or so, and a hand-over from warp to
-// warp costs some 200.  Forms that shared every tile between the warpgroups, 64
-// keys each, took 2850 cycles a tile (two waits and two arrivals a warp, the
-// scales of 64 keys against those of 128), with one O and a maximum handed from
-// warpgroup to warpgroup 3200.
+// arrival (of P).  A warpgroup takes 2250 cycles for a tile's 128 columns (1515
+// for a warp alone on its scheduler, of which the exponentials are 1024), its PV
+// and the next QK with the hand-overs 1790, in turn; the two warpgroups overlap,
+// which makes 2020 cycles a tile.  The products alone would be 1024, HBM at the
+// measured rate 1385.  Also built: one O, the maximum handed from warpgroup to
+// warpgroup, room for a third S (1830 cycles a tile, but every raise of the
+// maximum stops both; slower over a whole call); every tile shared by the
+// warpgroups, 64 keys each (2850: twice the waits and arrivals a key, some 200
+// cycles each); a quarter of the exponentials on the FMA pipe (no gain).
+// Measured: 16 sequences over 8192 keys, 32 query heads on 8, blocks of 32, d =
+// 128: 84 us, 3.3 TB/s and 820 TFLOP/s (bf16 counting: QK runs as two products
+// of half the price); 101 us where calls in a row hold the card at its power
+// limit, 1650 MHz.
 #pragma once
 
 #include "attn_tc_persist.cuh"
@@ -65,11 +72,11 @@ static_assert(kQtSmemBytes <= 227 * 1024, "more shared memory than a CTA may hav
 // part than there are tiles, so that the merge of a short launch walks over no
 // empty pieces.  Units stay whole only where the longest is at most 3 tiles
 // above the mean of the CTAs, about what merging costs.  And a range is not so
-// many tiles, but so much work: in front of each unit's tiles lie kHead
-// positions for what a segment costs besides its tiles.
-template <int HEAD>
+// many tiles, but so much work: behind each unit's tiles lie TAIL positions for
+// what a segment costs besides its tiles (verification over 64 ragged prefixes,
+// CTAs with 2 to 10 segments: 206 us without, 178 us with 4 to 6).
+template <int TAIL>
 struct QtSource {
-    static constexpr int kHead = HEAD;
     long long t, t1, t0, T; // positions: next, end and start of this CTA's, all
     long long seq_base;
     int seq, seq_tiles, len, G;
@@ -96,7 +103,7 @@ struct QtSource {
         return i < p.B ? max(0, decode_unit_tiles(len, p.b, p.nkeys, p.mode)) : 0;
     }
     // positions of a unit of so many tiles
-    __device__ static int span(int tiles) { return tiles ? tiles + kHead : 0; }
+    __device__ static int span(int tiles) { return tiles ? tiles + TAIL : 0; }
     __device__ void init(const PParams &p)
     {
         const int lane = threadIdx.x & 31;
@@ -170,14 +177,15 @@ struct QtSource {
                 seq_base += (long long)ups * span(seq_tiles);
                 seq_tiles = tiles_of(p, ++seq, len);
             }
-            int at; // position in the unit `uis` of the sequence
-            const int uis = divmod(t - seq_base, span(seq_tiles), at);
-            const int kt0 = max(at - kHead, 0);
-            const int n = (int)min((long long)(span(seq_tiles) - at), t1 - t) - (kt0 - at + kHead);
-            const long long u0 = t - at + kHead; // position of the unit's first tile
-            t = t - at + kHead + kt0 + max(n, 0);
-            if (n <= 0) // the range ends in front of the unit's first tile
-                return false;
+            int kt0; // first tile in the unit `uis` of the sequence
+            const int uis = divmod(t - seq_base, span(seq_tiles), kt0);
+            const long long u0 = t - kt0; // the unit's first position
+            if (kt0 >= seq_tiles) { // behind its tiles
+                t = u0 + span(seq_tiles);
+                continue;
+            }
+            const int n = (int)min((long long)(seq_tiles - kt0), t1 - t);
+            t += n;
             const int g = uis / p.row_tiles, rt = uis % p.row_tiles;
             sg.kvhead = seq * p.Hkv + g;
             sg.qrow0 = rt * kTcM;
@@ -244,8 +252,11 @@ __device__ __forceinline__ float lg2(float x)
 }
 
 // P reaches 2^kQtTop where the maximum was last raised, and 2^(kQtTop +
-// kQtLazy) before it is raised again: the largest f16 is above 2^15, and the
-// smallest normal one then 2^-20 of the row's largest P.
+// kQtLazy) before it is raised again.  2^15 is the largest power of two in f16;
+// from 2^-17 of the largest P on, at worst, the smaller ones are rounded to
+// multiples of 2^-27 of it, which over 2^15 keys stays below the rounding of the
+// larger ones.  A raise stops the warpgroup for some 1000 cycles: with 6 and 8,
+// heads of large scores took 1.3 us a tile where others took 1.1.
 constexpr float kQtTop = 3.f, kQtLazy = 12.f;
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)

@@ -21,7 +21,8 @@ extern "C" {
 
 /*
  * Arms a one-shot fault on the current device: in the next launch of the
- * tcgen05 kernel (bd_attn_fwd or bd_attn_decode with d = 128 or 64), CTA 0
+ * tcgen05 kernel (bd_attn_fwd, bd_attn_decode, or bd_attn_decode_q8 with more
+ * query rows a kv-head than its kernel for few rows takes), CTA 0
  * skips the copy of its first K tile, so the wait for that tile runs out
  * after about two seconds and the launch reports BD_ERR_DEVICE_TIMEOUT.
  * The outputs of that launch are undefined; later launches are unaffected.

@@ -459,6 +459,19 @@ def test_decode_bad_length_is_reported():
         assert torch.isfinite(lse[0]).all() and torch.isfinite(lse[2]).all()
 
 
+def test_decode_wait_that_runs_out_is_reported():
+    """One K tile never arrives: the bounded wait runs out, the launch reports
+    it, the next one is right."""
+    lens = [900, 300]
+    q, kv = decode_case(2, 4, 1, 20, 128, 1000, 64, lens, 0, 89)
+    (kc, ks), (vc, vs) = kv
+    assert bd.bd_attn_debug_inject_fault(1) == bd.BD_OK
+    bd.decode_q8(q.cuda(), cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 0, 64)
+    torch.cuda.synchronize()
+    assert bd.device_status() == bd.BD_ERR_DEVICE_TIMEOUT
+    run_decode(q, kv, lens, 0, 64)
+
+
 def test_decode_is_deterministic_and_takes_a_workspace_and_a_stream():
     lens = [900, 5, 260]
     q, kv = decode_case(3, 8, 2, 20, 128, 1000, 128, lens, 1, 83)
