@@ -131,6 +131,42 @@ __global__ void __launch_bounds__(kQrThreads, 1)
     };
     for (int i = 0; more && i < kQrStages; ++i)
         fill(nx, i);
+    // The queries of a segment as they lie, rows g and g + 8 of each 16, and the
+    // scales of this warp's first 32 keys: loaded before the segment's start, so
+    // that they are on their way while the one before is merged.
+    uint2 qw[MT][2][DH / 16];
+    auto load_queries = [&](const Seg &s) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = mt * 16 + h * 8 + g;
+                const bool valid = r < s.nrows;
+                const uint2 *row = reinterpret_cast<const uint2 *>(
+                    p.q + ((size_t)s.out_row0 + (valid ? r : 0)) * DH + t * (DH / 4));
+#pragma unroll
+                for (int i = 0; i < DH / 16; ++i)
+                    qw[mt][h][i] = valid ? row[i] : make_uint2(0, 0);
+            }
+    };
+    // scales of a 32-key part, two runs of 16 keys; keys that are none take
+    // neutral ones
+    auto scales = [&](const Seg &s, int k0, float2 *e) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int key = k0 + 16 * c;
+            e[c] = make_float2(1.f, 1.f);
+            if (key < s.hi0) {
+                const size_t at = (size_t)s.kvhead * p.groups + (key >> p.tshift);
+                e[c] = make_float2(p.ks[at], p.vs[at]);
+            }
+        }
+    };
+    float2 es[2];
+    if (more) {
+        load_queries(nx);
+        scales(nx, nx.lo0 + warp * KS, es);
+    }
 
     while (more) {
         sg = nx;
@@ -144,18 +180,13 @@ __global__ void __launch_bounds__(kQrThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = mt * 16 + h * 8 + g;
-                const bool valid = r < sg.nrows;
-                const uint2 *row = reinterpret_cast<const uint2 *>(
-                    p.q + ((size_t)sg.out_row0 + (valid ? r : 0)) * DH + t * (DH / 4));
-                uint2 w[DH / 16];
                 float amax = 0.f;
                 bool finite = true;
 #pragma unroll
                 for (int i = 0; i < DH / 16; ++i) {
-                    w[i] = valid ? row[i] : make_uint2(0, 0);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint32_t v = x ? w[i].y : w[i].x;
+                        const uint32_t v = x ? qw[mt][h][i].y : qw[mt][h][i].x;
                         const float a = fabsf(__uint_as_float(v << 16));
                         const float b = fabsf(__uint_as_float(v & 0xffff0000u));
                         finite = finite && a < INFINITY && b < INFINITY;
@@ -171,17 +202,15 @@ __global__ void __launch_bounds__(kQrThreads, 1)
                 qs[mt][h] = exp2_int(k);
 #pragma unroll
                 for (int i = 0; i < DH / 16; ++i) {
-                    qf[mt][i][h] = pack_f16x2(__uint_as_float(w[i].x << 16) * inv,
-                                              __uint_as_float(w[i].x & 0xffff0000u) * inv);
-                    qf[mt][i][2 + h] = pack_f16x2(__uint_as_float(w[i].y << 16) * inv,
-                                                  __uint_as_float(w[i].y & 0xffff0000u) * inv);
+                    qf[mt][i][h] = pack_f16x2(__uint_as_float(qw[mt][h][i].x << 16) * inv,
+                                              __uint_as_float(qw[mt][h][i].x & 0xffff0000u) * inv);
+                    qf[mt][i][2 + h] = pack_f16x2(__uint_as_float(qw[mt][h][i].y << 16) * inv,
+                                                  __uint_as_float(qw[mt][h][i].y & 0xffff0000u) * inv);
                 }
                 const int jr = min(r, sg.nrows - 1) % p.pp.b; // (one tile of rows a unit)
                 seen[mt][h] = min(sg.hi0, sg.len + (p.pp.mode == 0 ? p.pp.b : p.pp.mode == 1 ? jr + 1 : 0));
             }
         const int full_end = min(sg.fhi0, sg.hi0); // keys that every row sees
-        const float *ks_g = p.ks + (size_t)sg.kvhead * p.groups;
-        const float *vs_g = p.vs + (size_t)sg.kvhead * p.groups;
 
         float o[MT][NT][4];
         float m[MT][2], l[MT][2];
@@ -195,22 +224,6 @@ __global__ void __launch_bounds__(kQrThreads, 1)
             m[mt][0] = m[mt][1] = -INFINITY;
             l[mt][0] = l[mt][1] = 0.f;
         }
-        // scales of a 32-key part, two runs of 16 keys; keys that are none
-        // take neutral ones
-        auto scales = [&](int k0, float2 *e) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int key = k0 + 16 * c;
-                e[c] = make_float2(1.f, 1.f);
-                if (key < sg.hi0) {
-                    const int gr = key >> p.tshift;
-                    e[c] = make_float2(ks_g[gr], vs_g[gr]);
-                }
-            }
-        };
-        float2 es[2];
-        scales(sg.lo0 + warp * KS, es);
-
         for (int i = 0;; ++i) {
             const int k0 = sg.lo0 + (i * kQrWarps + warp) * KS;
             if (k0 >= sg.hi0)
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kQrThreads, 1)
                     break;
                 const float2 ec[2] = {es[0], es[1]};
                 // the next part's scales are on their way meanwhile
-                scales(part + 1 < KS / 32 ? ks + 32 : k0 + kQrWarps * KS, es);
+                scales(sg, part + 1 < KS / 32 ? ks + 32 : k0 + kQrWarps * KS, es);
                 // S = Q K^T, 8 keys at a time
                 float s[MT][4][4];
 #pragma unroll
@@ -339,6 +352,10 @@ __global__ void __launch_bounds__(kQrThreads, 1)
         more = src.next(p.pp, nx);
         for (int i = 0; more && i < kQrStages; ++i)
             fill(nx, i);
+        if (more) {
+            load_queries(nx);
+            scales(nx, nx.lo0 + warp * KS, es);
+        }
 
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) { // 16 rows at a time
