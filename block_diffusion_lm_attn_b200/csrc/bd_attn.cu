@@ -448,14 +448,14 @@ bd_status launch_q8_tc(const CUtensorMap &mk, const CUtensorMap &mv, const bd::Q
     }
 }
 
-template <int DH, int MT>
+template <int DH, int R>
 bd_status launch_q8_rows(const CUtensorMap &mk, const CUtensorMap &mv, const bd::QtParams &p,
                          int grid, cudaStream_t st)
 {
-    constexpr int smem = bd::kQrSmemBytes;
-    if (set_smem<bd::bd_decode_q8_rows_kernel<DH, MT>>(smem) != BD_OK)
+    constexpr int smem = bd::Qr<R>::kBytes;
+    if (set_smem<bd::bd_decode_q8_rows_kernel<DH, R>>(smem) != BD_OK)
         return BD_ERR_CUDA;
-    bd::bd_decode_q8_rows_kernel<DH, MT><<<grid, bd::kQrThreads, smem, st>>>(mk, mv, p);
+    bd::bd_decode_q8_rows_kernel<DH, R><<<grid, bd::kQrThreads, smem, st>>>(mk, mv, p);
     return cudaGetLastError() == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 
@@ -478,13 +478,13 @@ bd_status launch_q8(const void *k_cache, const void *v_cache, const bd::QtParams
                           : launch_dependent(bd::bd_decode_q8_combine_kernel<DH>, dim3(grid, 4),
                                              16 * DH / 8, p.pp, st);
     }
-    bd_status r;
-    if constexpr (q8_few_rows(DH) > 16) {
-        r = p.pp.rows_unit <= 16 ? launch_q8_rows<DH, 1>(mk, mv, p, grid, st)
-                                 : launch_q8_rows<DH, 2>(mk, mv, p, grid, st);
-    } else {
-        r = launch_q8_rows<DH, 1>(mk, mv, p, grid, st);
-    }
+    bd_status r = BD_OK;
+    if (p.pp.rows_unit <= 8)
+        r = launch_q8_rows<DH, 8>(mk, mv, p, grid, st);
+    else if (p.pp.rows_unit <= 16)
+        r = launch_q8_rows<DH, 16>(mk, mv, p, grid, st);
+    else if constexpr (q8_few_rows(DH) == 32)
+        r = launch_q8_rows<DH, 32>(mk, mv, p, grid, st);
     return r != BD_OK ? r : launch_combine<true>(p.pp, grid, st);
 }
 

@@ -317,9 +317,9 @@ def test_decode_head_groups_and_block_sizes(Hq, H, b):
 
 
 @pytest.mark.parametrize("d,group", [(128, 64), (128, 16), (64, 128), (64, 32), (32, 16), (32, 128)])
-@pytest.mark.parametrize("Hq,H,b", [(4, 1, 1), (3, 1, 5), (4, 2, 8), (4, 1, 5), (8, 2, 8), (1, 1, 31)])
+@pytest.mark.parametrize("Hq,H,b", [(4, 1, 1), (4, 2, 4), (3, 1, 3), (3, 1, 5), (4, 2, 8), (4, 1, 5), (8, 2, 8), (1, 1, 31)])
 def test_decode_few_rows(Hq, H, b, d, group):
-    """Up to 16 and up to 32 query rows a unit, over prefixes that end inside
+    """Up to 8, 16 and 32 query rows a unit, over prefixes that end inside
     and at the end of a step, a part of one and a run of 16 keys."""
     for mode in (0, 1, 2):
         lens = [1, 33, 128, 255, 1100, 0 if mode == 2 else 64]
