@@ -20,27 +20,32 @@
 //                   take alternate key tiles, and the one without a segment's
 //                   last tile splits the next segment's queries meanwhile
 //   warp 8          the work list, TMA of K and V, cp.async of the scales
-//   warp 9          MMA issue: per tile its PV and the QK two tiles on
-//   warps 10, 11    V codes to f16
-// TMEM: S/P of even and of odd tiles (128 columns; P, f16, over its own S), an
-// O for each warpgroup (128).  Shared memory: Q (hi and lo, 16 KB each), four
-// stages of K and three of V (16 KB), two buffers of V in f16 (32 KB).
+//   warps 9, 10     issue of QK, of PV
+//   warps 12-15     V codes to f16
+// TMEM: S (128 columns), a P in f16 (64) and an O (128) for each warpgroup.
+// Shared memory: Q (hi and lo, 16 KB each), four stages of K and three of V (16
+// KB), two buffers of V in f16 (32 KB).
 //
-// Each warpgroup has an O, a running maximum and a sum of its own, joined in
-// the epilogue, so that a tile costs a softmax warp one wait (for S) and one
-// arrival (of P).  A warpgroup takes 2250 cycles for a tile's 128 columns (1515
-// for a warp alone on its scheduler, of which the exponentials are 1024), its PV
-// and the next QK with the hand-overs 1790, in turn; the two warpgroups overlap,
-// which makes 2020 cycles a tile.  The products alone would be 1024, HBM at the
-// measured rate 1385.  Also built: one O, the maximum handed from warpgroup to
-// warpgroup, room for a third S (1830 cycles a tile, but every raise of the
-// maximum stops both; slower over a whole call); every tile shared by the
-// warpgroups, 64 keys each (2850: twice the waits and arrivals a key, some 200
-// cycles each); a quarter of the exponentials on the FMA pipe (no gain).
+// S goes to registers at once, 128 a thread, and with it read the next QK may run:
+// one S serves both warpgroups.  Each has an O, a running maximum and a sum of
+// its own, joined in the epilogue, so that no tile waits for another's softmax.
+//
+// Bound: a tile takes 1900 cycles.  Its exponentials alone are 1024 (the two
+// warpgroups' overlap and take 1980 together), its products 1150, its shared-memory
+// traffic of 176 KB 1400, its bytes at the measured HBM rate 1385; without the
+// exponentials, without the conversion, with half of either product it would
+// still be 1750 to 1800 each: what is left are hand-overs, 100 to 250 cycles each.
+// Calls in a row are bound by the card's power: 1600 MHz.  Also built: S and P in
+// the same columns with two S, one warp for both products, two for the
+// conversion (2 us more, of 81); one O, the maximum handed from warpgroup to
+// warpgroup (every raise of it stops both); every tile shared by the warpgroups,
+// 64 keys each (twice the waits and arrivals a key); a quarter of the
+// exponentials on the FMA pipe, or integer operations for the conversion (no
+// gain, and 2 us more).
 // Measured: 16 sequences over 8192 keys, 32 query heads on 8, blocks of 32, d =
-// 128: 84 us, 3.3 TB/s and 820 TFLOP/s (bf16 counting: QK runs as two products
-// of half the price); 101 us where calls in a row hold the card at its power
-// limit, 1650 MHz.
+// 128: 78 us, 3.5 TB/s and 880 TFLOP/s (bf16 counting: QK runs as two products
+// of half the price); 94 us where calls in a row hold the card at its power
+// limit.
 #pragma once
 
 #include "attn_tc_persist.cuh"
@@ -48,7 +53,7 @@
 
 namespace bd {
 
-constexpr int kQtThreads = 384;
+constexpr int kQtThreads = 512;
 constexpr int kQtTile = kTcN * kTcD; // bytes of a key tile's codes
 constexpr int kQtKStages = 4, kQtVStages = 3;
 
@@ -70,8 +75,11 @@ static_assert(kQtSmemBytes <= 227 * 1024, "more shared memory than a CTA may hav
 // reads 32 lengths at a time (one after another they took 3 us for 16
 // sequences and 8 us for 64, at the head of every launch).  No more CTAs take
 // part than there are tiles, so that the merge of a short launch walks over no
-// empty pieces.  Units stay whole only where the longest is at most 3 tiles
-// above the mean of the CTAs, about what merging costs.  And a range is not so
+// empty pieces.  Units stay whole where the longest is at most 12 tiles above
+// the mean of the CTAs, about what a second segment and the merge cost (blocks of
+// 32 over 8192 keys, d = 128, 15 and 16 sequences of 8 kv-heads, 12.3 and 8.8
+// tiles above: whole 77.1 and 78.0 us, cut 76.1 and 80.5; one sequence of 2
+// kv-heads, 777 keys, d = 64, 6 above: 8.5 and 10.5).  And a range is not so
 // many tiles, but so much work: behind each unit's tiles lie TAIL positions for
 // what a segment costs besides its tiles (verification over 64 ragged prefixes,
 // CTAs with 2 to 10 segments: 206 us without, 178 us with 4 to 6).
@@ -133,7 +141,7 @@ struct QtSource {
         G = (int)min((long long)gridDim.x, max(tiles, 1LL));
         t = t0 = t1 = seq_base = 0;
         seq = seq_tiles = len = 0;
-        if (units <= gridDim.x && (long long)(maxt - 3) * G <= tiles) {
+        if (units <= gridDim.x && (long long)(maxt - 12) * G <= tiles) {
             // CTA c takes unit c
             if (blockIdx.x < units) {
                 seq = blockIdx.x / ups;
@@ -382,13 +390,14 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     auto bar_vempty = [&](int s) { return bar0 + 88 + 8 * s; };
     auto bar_ifull = [&](int s) { return bar0 + 112 + 8 * s; };  // segment si & 3
     auto bar_iempty = [&](int s) { return bar0 + 144 + 8 * s; };
-    auto bar_sfull = [&](int w) { return bar0 + 176 + 8 * w; };  // S of tile j & 1
+    auto bar_sfull = [&](int w) { return bar0 + 176 + 8 * w; };  // S, of a tile j with j & 1 = w
     auto bar_pv = [&](int w) { return bar0 + 192 + 8 * w; };     // its P, its V in f16
     auto bar_odone = [&](int w) { return bar0 + 208 + 8 * w; };  // its PV done
     auto bar_qfull = [&](int s) { return bar0 + 224 + 8 * s; };  // queries of segment si & 1
     const uint32_t bar_l = bar0 + 240;     // both sums of a segment written
     const uint32_t bar_ofree = bar0 + 248; // both O read out
     const uint32_t bar_final = bar0 + 256;
+    const uint32_t bar_sfree = bar0 + 264; // S read by its warpgroup
     static_assert(kQtKStages == 4 && kQtVStages == 3, "barrier layout");
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 272);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 280);
@@ -404,21 +413,22 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             mbar_init(bar_kfull(s), 1 + 2 * NG); // + a copy of each scale
             mbar_init(bar_kempty(s), 1);
             mbar_init(bar_ifull(s), 1);
-            mbar_init(bar_iempty(s), 11); // 8 softmax warps, MMA, 2 converters
+            mbar_init(bar_iempty(s), 14); // 8 softmax warps, QK, PV, 4 converters
         }
         for (int s = 0; s < 3; ++s) {
             mbar_init(bar_vfull(s), 1);
-            mbar_init(bar_vempty(s), 2);
+            mbar_init(bar_vempty(s), 4);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar_sfull(w), 1);
-            mbar_init(bar_pv(w), 4 + 2); // softmax warps, converters
+            mbar_init(bar_pv(w), 4 + 4); // softmax warps, converters
             mbar_init(bar_odone(w), 1);
             mbar_init(bar_qfull(w), 4);
         }
         mbar_init(bar_l, 256);
         mbar_init(bar_ofree, 8);
-        mbar_init(bar_final, 1);
+        mbar_init(bar_final, 2);
+        mbar_init(bar_sfree, 4);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t t_o = tmem + 256;
+    const uint32_t t_p = tmem + 128, t_o = tmem + 256; // 64 and 128 columns a warpgroup
     // the combine kernel may be scheduled now; it reads nothing of this
     // launch before the whole grid has finished
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -442,242 +452,258 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     // a barrier wait by a converged warp
     auto wait = [&](uint32_t bar, uint32_t parity) { return qt_wait(bar, parity, abort_flag); };
 
-    if (warp == 8) {
-        // -------------------------- work list; loads of K, V and the scales
-        QtSource<5> src;
-        src.init(p.pp);
-        if (lane == 0)
-            p.pp.cut_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-        Seg sg;
-        bool ok = true;
-        int g = 0, vs = 0;           // running tile counter, its V stage
-        uint32_t vpar = 1;           // parity of the wait for that stage
-        int kiss = 0, viss = 0;      // tiles issued
-        for (int si = 0; ok; ++si) {
-            const int slot = si & 3;
-            if (si >= 4 && !(ok = wait(bar_iempty(slot), (uint32_t)(((si - 4) >> 2) & 1))))
-                break;
-            const bool got = src.next(p.pp, sg);
-            if (lane == 0) {
-                if (got)
-                    seg_ring[slot] = sg;
-                else
-                    seg_ring[slot].nt = 0;
-                mbar_arrive(bar_ifull(slot));
-            }
-            __syncwarp();
-            if (!got)
-                break;
-            // its queries, which a warpgroup reads when the segment before is
-            // all but done
-            if (si > 0)
-                for (int e = lane * 128; e < sg.nrows * DH * 2; e += 32 * 128)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                        reinterpret_cast<const char *>(p.q + (size_t)sg.out_row0 * DH) + e));
-            for (int it = 0; it < sg.nt; ++it, ++g) {
-                const int ks = sg.lo0 + it * kTcN, s = g & 3;
-                if (g >= 4 && !(ok = wait(bar_kempty(s), (uint32_t)((g >> 2) & 1) ^ 1u)))
-                    break;
-                // injected fault: this tile never arrives
-                const bool skip = g == 0 && blockIdx.x == 0 && lane == 0 &&
-                                  atomicExch(&g_fault_skip_k, 0) != 0;
-                if (lane == 0 && !skip) {
-                    mbar_expect_tx(bar_kfull(s), kQtTile);
-                    tma_load_3d(base + kQtSmemK + s * kQtTile, &tm_k, 0, ks, sg.kvhead, bar_kfull(s));
-                    kiss = g + 1;
-                }
-                // Scales: one lane each, K's first.  Groups with no visible key
-                // give 0, which no visible score is multiplied by.  A slot is
-                // taken again 8 tiles on, behind QK_{g-4} and so behind the
-                // softmax of tile g - 6.
-                if (lane < 2 * NG) {
-                    const int key = ks + (kTcN / NG) * (lane % NG);
-                    const bool in = key < sg.hi0;
-                    const float *from = (lane < NG ? p.ks : p.vs) + (size_t)sg.kvhead * p.groups +
-                                        (in ? key / (kTcN / NG) : 0);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                     base + kQtSmemSc + (g & 7) * 64 + (lane / NG) * 32 + (lane % NG) * 4),
-                                 "l"(from), "r"(in ? 4 : 0)
-                                 : "memory");
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                                     bar_kfull(s))
-                                 : "memory");
-                }
-                if (g >= kQtVStages && !(ok = wait(bar_vempty(vs), vpar)))
-                    break;
-                if (lane == 0) {
-                    mbar_expect_tx(bar_vfull(vs), kQtTile);
-                    tma_load_3d(base + kQtSmemV + vs * kQtTile, &tm_v, 0, ks, sg.kvhead, bar_vfull(vs));
-                    viss = g + 1;
-                }
-                __syncwarp();
-                if (++vs == kQtVStages) {
-                    vs = 0;
-                    vpar ^= 1;
-                }
-            }
-        }
-        // wait (bounded) for every copy this role issued
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (lane == 0) {
-            const long long c0 = clock64();
-            for (int x = max(kiss - kQtKStages, 0); x < kiss; ++x)
-                while (!mbar_try_wait(bar_kfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
-                       clock64() - c0 < kWaitCycles) {}
-            for (int x = max(viss - kQtVStages, 0); x < viss; ++x)
-                while (!mbar_try_wait(bar_vfull(x % kQtVStages), (uint32_t)((x / kQtVStages) & 1)) &&
-                       clock64() - c0 < kWaitCycles) {}
-        }
-    } else if (warp == 9) {
-        // ---------------------------------------------------- MMA issue
-        const uint32_t ld = elect_one();
-        constexpr uint32_t idesc_qk = idesc_fmt0(kTcM, kTcN, 0);
-        // O has DH columns; a 64-column half of V at least
-        constexpr uint32_t idesc_pv = idesc_fmt0(kTcM, DH > 64 ? 128 : 64, 1);
-        bool ok = true;
-        // K of tile j is there
-        auto have_k = [&](int j) { return ok = wait(bar_kfull(j & 3), (uint32_t)((j >> 2) & 1)); };
-        // QK of tile j.  Its S buffer held P of tile j - 2, whose PV was
-        // issued before.
-        auto qk = [&](int j) {
-            const uint32_t ts = tmem + (uint32_t)(j & 1) * kTcN;
-            const uint32_t qb = base + kQtSmemQ, kb = base + kQtSmemK + (uint32_t)(j & 3) * kQtTile;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int kk = 0; kk < DH / 32; ++kk)
-                    tc_mma8_ss_p(ts, smem_desc_sw128(qb + h * kQtTile + kk * 32, 16, 1024),
-                                 smem_desc_sw128(kb + kk * 32, 16, 1024), idesc_qk,
-                                 h || kk ? 1u : 0u, ld);
-            tc_commit_p(bar_sfull(j & 1), ld);
-            tc_commit_p(bar_kempty(j & 3), ld);
-        };
-        int j = 0;
-        for (int si = 0; ok; ++si) {
-            if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
-                break;
-            const int n = seg_ring[si & 3].nt;
-            if (n == 0 || !(ok = wait(bar_qfull(si & 1), (uint32_t)((si >> 1) & 1))))
-                break;
-            for (int i = 0; i < min(n, 2); ++i) {
-                if (!have_k(j + i))
-                    break;
-                tc_fence_after();
-                qk(j + i);
-            }
-            // O was last read out by the epilogue of segment si - 1
-            if (!ok || (si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1)))))
-                break;
-            for (int i = 0; i < n; ++i, ++j) {
-                const int w = j & 1;
-                // (K first: it has been there for long, and nothing is to stand
-                // between the PV and the QK behind it)
-                if ((i + 2 < n && !have_k(j + 2)) || !(ok = wait(bar_pv(w), (uint32_t)((j >> 1) & 1))))
-                    break;
-                tc_fence_after();
-                const uint32_t vb = base + kQtSmemW + (uint32_t)w * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < kTcN / 16; ++kk)
-                    tc_mma_ts_p(t_o + w * 128, tmem + w * kTcN + kk * 8,
-                                smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024), idesc_pv,
-                                (i > 1 || kk > 0) ? 1u : 0u, ld);
-                tc_commit_p(bar_odone(w), ld);
-                if (i + 2 < n)
-                    qk(j + 2);
-            }
-            __syncwarp();
-            if (ok && lane == 0)
-                mbar_arrive(bar_iempty(si & 3));
-        }
+    // the end of a warp that issued products: wait (bounded) for all of both
+    auto drain = [&](uint32_t ld) {
         tc_commit_p(bar_final, ld);
         const long long c0 = clock64();
         while (!mbar_try_wait(bar_final, 0) && clock64() - c0 < kWaitCycles) {}
         __syncwarp();
-    } else if (warp >= 10) {
-        // ------------------------------------------------ V codes to f16
-        const int cw = warp - 10;
-        bool ok = true;
-        int j = 0, vs = 0;
-        uint32_t vpar = 0;
-        for (int si = 0; ok; ++si) {
-            if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
-                break;
-            const Seg &sg = seg_ring[si & 3];
-            const int nt = sg.nt, lo = sg.lo0, hi = sg.hi0;
-            __syncwarp();
-            if (nt == 0)
-                break;
+    };
+
+    // Registers: a softmax thread holds a row of S, 128.  2 x 128 x (184 + 72) is
+    // what the launch has, 512 x 128.
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+            // -------------------------- work list; loads of K, V and the scales
+            QtSource<5> src;
+            src.init(p.pp);
             if (lane == 0)
-                mbar_arrive(bar_iempty(si & 3));
-            for (int it = 0; it < nt; ++it, ++j) {
-                const int b = j & 1, ks = lo + it * kTcN;
-                // the f16 buffer was last read by the PV of tile j - 2
-                if (!(ok = wait(bar_vfull(vs), vpar)) ||
-                    (j >= 2 && !(ok = wait(bar_odone(b), (uint32_t)(((j - 2) >> 1) & 1)))))
+                p.pp.cut_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+            Seg sg;
+            bool ok = true;
+            int g = 0, vs = 0;           // running tile counter, its V stage
+            uint32_t vpar = 1;           // parity of the wait for that stage
+            int kiss = 0, viss = 0;      // tiles issued
+            for (int si = 0; ok; ++si) {
+                const int slot = si & 3;
+                if (si >= 4 && !(ok = wait(bar_iempty(slot), (uint32_t)(((si - 4) >> 2) & 1))))
                     break;
-                // 8 lanes take half a row each of rows r and r ^ 5 (64 codes
-                // = 4 vectors of 16): their reads of the swizzled codes and
-                // their writes of the swizzled halves each cover all banks.
-                const uint32_t src = base + kQtSmemV + (uint32_t)vs * kQtTile;
-                const uint32_t dst = base + kQtSmemW + (uint32_t)b * kTileBytes;
-                // rows of 8: pairs (0, 5), (2, 7), (4, 1), (6, 3)
-                const int hrow = (lane >> 3) * 2;
-                const int r8 = (lane & 4) ? (hrow ^ 5) : hrow;
-                const int u4 = lane & 3;
-                constexpr int H = DH <= 64 ? 1 : 2; // halves of 64 columns
-#pragma unroll 1
-                for (int rr = 64 * cw; rr < 64 * cw + 64; rr += 32) {
-                    uint32_t x[4 * H][4]; // all loads go out first
-#pragma unroll
-                    for (int i = 0; i < 4 * H; ++i) {
-                        const int r = rr + 8 * (i / H) + r8;
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
-                                     : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
-                                     : "memory");
-                    }
-                    if (ks + rr + 32 > hi) { // not keys: no code of theirs may be used
-#pragma unroll
-                        for (int i = 0; i < 4 * H; ++i)
-                            if (ks + rr + 8 * (i / H) + r8 >= hi)
-                                x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4 * H; ++i) {
-                        uint32_t y[8];
-#pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            y[t] = half2_of_e4m3x2((uint16_t)(x[i][t >> 1] >> (16 * (t & 1))));
-                        const uint32_t row = dst + (i % H) * kHalfTileBytes + (rr + 8 * (i / H) + r8) * 128;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         row + (((2 * u4) ^ r8) << 4)),
-                                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                     : "memory");
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         row + (((2 * u4 + 1) ^ r8) << 4)),
-                                     "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                                     : "memory");
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
+                const bool got = src.next(p.pp, sg);
                 if (lane == 0) {
-                    mbar_arrive(bar_pv(b));
-                    mbar_arrive(bar_vempty(vs));
+                    if (got)
+                        seg_ring[slot] = sg;
+                    else
+                        seg_ring[slot].nt = 0;
+                    mbar_arrive(bar_ifull(slot));
                 }
-                if (++vs == kQtVStages) {
-                    vs = 0;
-                    vpar ^= 1;
+                __syncwarp();
+                if (!got)
+                    break;
+                // its queries, which a warpgroup reads when the segment before is
+                // all but done
+                if (si > 0)
+                    for (int e = lane * 128; e < sg.nrows * DH * 2; e += 32 * 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                            reinterpret_cast<const char *>(p.q + (size_t)sg.out_row0 * DH) + e));
+                for (int it = 0; it < sg.nt; ++it, ++g) {
+                    const int ks = sg.lo0 + it * kTcN, s = g & 3;
+                    if (g >= 4 && !(ok = wait(bar_kempty(s), (uint32_t)((g >> 2) & 1) ^ 1u)))
+                        break;
+                    // injected fault: this tile never arrives
+                    const bool skip = g == 0 && blockIdx.x == 0 && lane == 0 &&
+                                      atomicExch(&g_fault_skip_k, 0) != 0;
+                    if (lane == 0 && !skip) {
+                        mbar_expect_tx(bar_kfull(s), kQtTile);
+                        tma_load_3d(base + kQtSmemK + s * kQtTile, &tm_k, 0, ks, sg.kvhead, bar_kfull(s));
+                        kiss = g + 1;
+                    }
+                    // Scales: one lane each, K's first.  Groups with no visible key
+                    // give 0, which no visible score is multiplied by.  A slot is
+                    // taken again 8 tiles on, behind QK_{g-4}, so behind the load
+                    // of S_{g-6} and the softmax of tile g - 8 before it.
+                    if (lane < 2 * NG) {
+                        const int key = ks + (kTcN / NG) * (lane % NG);
+                        const bool in = key < sg.hi0;
+                        const float *from = (lane < NG ? p.ks : p.vs) + (size_t)sg.kvhead * p.groups +
+                                            (in ? key / (kTcN / NG) : 0);
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                         base + kQtSmemSc + (g & 7) * 64 + (lane / NG) * 32 + (lane % NG) * 4),
+                                     "l"(from), "r"(in ? 4 : 0)
+                                     : "memory");
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                                         bar_kfull(s))
+                                     : "memory");
+                    }
+                    if (g >= kQtVStages && !(ok = wait(bar_vempty(vs), vpar)))
+                        break;
+                    if (lane == 0) {
+                        mbar_expect_tx(bar_vfull(vs), kQtTile);
+                        tma_load_3d(base + kQtSmemV + vs * kQtTile, &tm_v, 0, ks, sg.kvhead, bar_vfull(vs));
+                        viss = g + 1;
+                    }
+                    __syncwarp();
+                    if (++vs == kQtVStages) {
+                        vs = 0;
+                        vpar ^= 1;
+                    }
+                }
+            }
+            // wait (bounded) for every copy this role issued
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (lane == 0) {
+                const long long c0 = clock64();
+                for (int x = max(kiss - kQtKStages, 0); x < kiss; ++x)
+                    while (!mbar_try_wait(bar_kfull(x & 3), (uint32_t)((x >> 2) & 1)) &&
+                           clock64() - c0 < kWaitCycles) {}
+                for (int x = max(viss - kQtVStages, 0); x < viss; ++x)
+                    while (!mbar_try_wait(bar_vfull(x % kQtVStages), (uint32_t)((x / kQtVStages) & 1)) &&
+                           clock64() - c0 < kWaitCycles) {}
+            }
+        } else if (warp == 9) {
+            // ---------------------------------------------------- issue of QK
+            const uint32_t ld = elect_one();
+            constexpr uint32_t idesc_qk = idesc_fmt0(kTcM, kTcN, 0);
+            bool ok = true;
+            int j = 0;
+            for (int si = 0; ok; ++si) {
+                if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
+                    break;
+                const int n = seg_ring[si & 3].nt;
+                if (n == 0 || !(ok = wait(bar_qfull(si & 1), (uint32_t)((si >> 1) & 1))))
+                    break;
+                for (int i = 0; i < n; ++i, ++j) {
+                    // K is there, and S of tile j - 1 has been read
+                    if (!(ok = wait(bar_kfull(j & 3), (uint32_t)((j >> 2) & 1))) ||
+                        (j > 0 && !(ok = wait(bar_sfree, (uint32_t)((j - 1) & 1)))))
+                        break;
+                    tc_fence_after();
+                    const uint32_t qb = base + kQtSmemQ, kb = base + kQtSmemK + (uint32_t)(j & 3) * kQtTile;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int kk = 0; kk < DH / 32; ++kk)
+                            tc_mma8_ss_p(tmem, smem_desc_sw128(qb + h * kQtTile + kk * 32, 16, 1024),
+                                         smem_desc_sw128(kb + kk * 32, 16, 1024), idesc_qk,
+                                         h || kk ? 1u : 0u, ld);
+                    tc_commit_p(bar_sfull(j & 1), ld);
+                    tc_commit_p(bar_kempty(j & 3), ld);
+                }
+                __syncwarp();
+                if (ok && lane == 0)
+                    mbar_arrive(bar_iempty(si & 3));
+            }
+            drain(ld);
+        } else if (warp == 10) {
+            // ---------------------------------------------------- issue of PV
+            const uint32_t ld = elect_one();
+            // O has DH columns; a 64-column half of V at least
+            constexpr uint32_t idesc_pv = idesc_fmt0(kTcM, DH > 64 ? 128 : 64, 1);
+            bool ok = true;
+            int j = 0;
+            for (int si = 0; ok; ++si) {
+                if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
+                    break;
+                const int n = seg_ring[si & 3].nt;
+                // O was last read out by the epilogue of segment si - 1
+                if (n == 0 || (si >= 1 && !(ok = wait(bar_ofree, (uint32_t)((si - 1) & 1)))))
+                    break;
+                for (int i = 0; i < n; ++i, ++j) {
+                    const int w = j & 1;
+                    if (!(ok = wait(bar_pv(w), (uint32_t)((j >> 1) & 1))))
+                        break;
+                    tc_fence_after();
+                    const uint32_t vb = base + kQtSmemW + (uint32_t)w * kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kTcN / 16; ++kk)
+                        tc_mma_ts_p(t_o + w * 128, t_p + w * 64 + kk * 8,
+                                    smem_desc_sw128(vb + kk * 2048, kHalfTileBytes, 1024), idesc_pv,
+                                    (i > 1 || kk > 0) ? 1u : 0u, ld);
+                    tc_commit_p(bar_odone(w), ld);
+                }
+                __syncwarp();
+                if (ok && lane == 0)
+                    mbar_arrive(bar_iempty(si & 3));
+            }
+            drain(ld);
+        } else if (warp >= 12) {
+            // ------------------------------------------------ V codes to f16
+            const int cw = warp - 12;
+            bool ok = true;
+            int j = 0, vs = 0;
+            uint32_t vpar = 0;
+            for (int si = 0; ok; ++si) {
+                if (!(ok = wait(bar_ifull(si & 3), (uint32_t)((si >> 2) & 1))))
+                    break;
+                const Seg &sg = seg_ring[si & 3];
+                const int nt = sg.nt, lo = sg.lo0, hi = sg.hi0;
+                __syncwarp();
+                if (nt == 0)
+                    break;
+                if (lane == 0)
+                    mbar_arrive(bar_iempty(si & 3));
+                for (int it = 0; it < nt; ++it, ++j) {
+                    const int b = j & 1, ks = lo + it * kTcN;
+                    // the f16 buffer was last read by the PV of tile j - 2
+                    if (!(ok = wait(bar_vfull(vs), vpar)) ||
+                        (j >= 2 && !(ok = wait(bar_odone(b), (uint32_t)(((j - 2) >> 1) & 1)))))
+                        break;
+                    // 8 lanes take half a row each of rows r and r ^ 5 (64 codes
+                    // = 4 vectors of 16): their reads of the swizzled codes and
+                    // their writes of the swizzled halves each cover all banks.
+                    const uint32_t src = base + kQtSmemV + (uint32_t)vs * kQtTile;
+                    const uint32_t dst = base + kQtSmemW + (uint32_t)b * kTileBytes;
+                    // rows of 8: pairs (0, 5), (2, 7), (4, 1), (6, 3)
+                    const int hrow = (lane >> 3) * 2;
+                    const int r8 = (lane & 4) ? (hrow ^ 5) : hrow;
+                    const int u4 = lane & 3;
+                    constexpr int H = DH <= 64 ? 1 : 2; // halves of 64 columns
+#pragma unroll 1
+                    for (int rr = 32 * cw; rr < 32 * cw + 32; rr += 32) {
+                        uint32_t x[4 * H][4]; // all loads go out first
+#pragma unroll
+                        for (int i = 0; i < 4 * H; ++i) {
+                            const int r = rr + 8 * (i / H) + r8;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
+                                         : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
+                                         : "memory");
+                        }
+                        if (ks + rr + 32 > hi) { // not keys: no code of theirs may be used
+#pragma unroll
+                            for (int i = 0; i < 4 * H; ++i)
+                                if (ks + rr + 8 * (i / H) + r8 >= hi)
+                                    x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4 * H; ++i) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int t = 0; t < 8; ++t)
+                                y[t] = half2_of_e4m3x2((uint16_t)(x[i][t >> 1] >> (16 * (t & 1))));
+                            const uint32_t row = dst + (i % H) * kHalfTileBytes + (rr + 8 * (i / H) + r8) * 128;
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             row + (((2 * u4) ^ r8) << 4)),
+                                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                         : "memory");
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             row + (((2 * u4 + 1) ^ r8) << 4)),
+                                         "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                                         : "memory");
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar_pv(b));
+                        mbar_arrive(bar_vempty(vs));
+                    }
+                    if (++vs == kQtVStages) {
+                        vs = 0;
+                        vpar ^= 1;
+                    }
                 }
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------------- softmax and epilogue
         const int wg = warp >> 2;
         const int row = threadIdx.x & (kTcM - 1);
         const int wrow = row & ~31; // first row of this warp
         const uint32_t lane_off = (uint32_t)wrow << 16;
-        const uint32_t ts = tmem + wg * kTcN + lane_off;   // this warpgroup's S
+        const uint32_t ts = tmem + lane_off;
+        const uint32_t tp = t_p + wg * 64 + lane_off;    // this warpgroup's P
         const uint32_t t_ow = t_o + wg * 128 + lane_off;   // and O
         // The queries of segment si, by one warpgroup, into the buffer that
         // no QK reads any more.
@@ -718,10 +744,17 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 const int j = j0 + i; // tile
                 if (!(ok = wait(bar_sfull(wg), (uint32_t)((j >> 1) & 1))))
                     break;
+                // PV_{j-2}, which reads P and writes O.  (It is waited for here by
+                // every warp and for every tile: no phase can be mistaken.)
+                auto prev_done = [&] { return ok = i < 2 || wait(bar_odone(wg), (uint32_t)(((j - 2) >> 1) & 1)); };
                 if (live) {
                     tc_fence_after();
                     uint32_t sr[kTcN];
                     tmem_ld32x4_wait(ts, ts + 32, ts + 64, ts + 96, sr, sr + 32, sr + 64, sr + 96);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar_sfree);
                     float s[kTcN];
 #pragma unroll
                     for (int c = 0; c < kTcN; ++c)
@@ -757,6 +790,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         }
                         mt = fmaxf(mt, fmaf(fmaxf(mc[0], mc[1]), ea[c], lg2(ev[c])));
                     }
+                    if (!prev_done())
+                        break;
+                    tc_fence_after();
                     const bool need = mt > m + (kQtTop + kQtLazy);
                     if (__any_sync(0xffffffffu, need)) {
                         float c = 1.f;
@@ -765,8 +801,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                             l = m == -INFINITY ? l : l * c; // 0, or NaN for good
                             m = mt - kQtTop;
                         }
-                        // The TMEM read-modify-write of O is warp-collective.
-                        // QK_j was issued behind PV_{j-2}, the last to write it.
+                        // the TMEM read-modify-write of O is warp-collective
                         if (i > 1) {
 #pragma unroll 1
                             for (int q4 = 0; q4 < DH / 16; ++q4) {
@@ -801,15 +836,20 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                             pk[x / 2 + 1] = pack_f16x2(y2, y3);
                             // stored 32 keys at a time (16: a group of them)
                             if (W >= 32 && (x & 31) == 28)
-                                tmem_st16(ts + c * (W / 2) + (x & ~31) / 2, pk + (x & ~31) / 2);
+                                tmem_st16(tp + c * (W / 2) + (x & ~31) / 2, pk + (x & ~31) / 2);
                         }
                         if (W == 16)
-                            tmem_st8(ts + c * 8, pk);
+                            tmem_st8(tp + c * 8, pk);
                         l = fmaf((r0 + r1) + (r2 + r3), 1.f / ev[c], l);
                     }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
+                } else {
+                    if (lane == 0)
+                        mbar_arrive(bar_sfree);
+                    if (!prev_done())
+                        break;
                 }
                 if (lane == 0)
                     mbar_arrive(bar_pv(wg));
@@ -825,8 +865,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 break;
             s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float2(l, m);
             mbar_arrive(bar_l);
-            // The last PV.  (The phase before on that barrier, PV_{jl-2}, is
-            // behind QK_jl, which every warp has seen.)
+            // The last PV.  (The phase before on that barrier, PV_{jl-2}, was
+            // waited for by the warpgroup of tile jl before it arrived here.)
             if (!(ok = wait(bar_l, (uint32_t)(si & 1))) ||
                 !(ok = wait(bar_odone(jl & 1), (uint32_t)((jl >> 1) & 1))))
                 break;
