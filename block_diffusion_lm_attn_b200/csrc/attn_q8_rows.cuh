@@ -566,6 +566,8 @@ __global__ void __launch_bounds__(kQrThreads, 1)
         if (!sg.complete && sg.last_cta >= 0 && threadIdx.x == 0)
             p.pp.cut_desc[blockIdx.x] = make_int4(sg.nrows, sg.last_cta, sg.out_row0, 0);
     }
+    if (p.whole)
+        q8_fill_empty_unit<DH>(p.pp);
     // wait (bounded) for copies that an aborted wait has left in flight
     const long long c0 = clock64();
     for (int x = max(issued - kQrStages, 0); x < issued; ++x)

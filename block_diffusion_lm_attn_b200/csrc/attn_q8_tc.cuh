@@ -83,6 +83,8 @@ static_assert(kQtSmemBytes <= 227 * 1024, "more shared memory than a CTA may hav
 // many tiles, but so much work: behind each unit's tiles lie TAIL positions for
 // what a segment costs besides its tiles (verification over 64 ragged prefixes,
 // CTAs with 2 to 10 segments: 206 us without, 178 us with 4 to 6).
+constexpr int kQtWhole = 12;
+
 template <int TAIL>
 struct QtSource {
     long long t, t1, t0, T; // positions: next, end and start of this CTA's, all
@@ -141,7 +143,7 @@ struct QtSource {
         G = (int)min((long long)gridDim.x, max(tiles, 1LL));
         t = t0 = t1 = seq_base = 0;
         seq = seq_tiles = len = 0;
-        if (units <= gridDim.x && (long long)(maxt - 12) * G <= tiles) {
+        if (units <= gridDim.x && (long long)(maxt - kQtWhole) * G <= tiles) {
             // CTA c takes unit c
             if (blockIdx.x < units) {
                 seq = blockIdx.x / ups;
@@ -223,7 +225,28 @@ struct QtParams {
     const bf16 *q;
     const float *ks, *vs; // [B * Hkv, groups]
     int groups, tshift;   // log2 of the positions per group
+    int whole;            // no unit can be cut: CTA c takes unit c, nothing is merged
 };
+
+// A unit without a key tile, by the CTA that has it, where no second kernel
+// fills such rows: an invalid length gives NaN rows, an empty prefix in mode 2
+// rows with no visible key (out 0, lse -inf).
+template <int DH> __device__ __forceinline__ void q8_fill_empty_unit(const PParams &p)
+{
+    const int ups = p.Hkv * p.row_tiles, seq = blockIdx.x / ups;
+    const int tiles = decode_unit_tiles(p.cache_len[seq], p.b, p.nkeys, p.mode);
+    if (tiles > 0)
+        return;
+    const int uis = blockIdx.x % ups, g = uis / p.row_tiles, rt = uis % p.row_tiles;
+    const size_t row0 = ((size_t)seq * p.Hq + g * (p.Hq / p.Hkv)) * p.b + rt * kTcM;
+    const int nrows = min(kTcM, p.rows_unit - rt * kTcM);
+    for (int e = threadIdx.x; e < nrows * DH; e += blockDim.x)
+        p.out[row0 * DH + e] = __float2bfloat16_rn(tiles < 0 ? NAN : 0.f);
+    for (int r = threadIdx.x; r < nrows; r += blockDim.x)
+        p.lse[row0 + r] = tiles < 0 ? NAN : -INFINITY;
+    if (threadIdx.x == 0 && tiles < 0)
+        raise_device_code(DEV_BAD_CACHE_LEN);
+}
 
 // D[tmem] (+)= A[smem desc] * B[smem desc] of e4m3 codes
 __device__ __forceinline__ void tc_mma8_ss_p(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -935,6 +958,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         }
     }
 
+    if (p.whole)
+        q8_fill_empty_unit<DH>(p.pp);
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {

@@ -459,6 +459,25 @@ def test_decode_bad_length_is_reported():
         assert torch.isfinite(lse[0]).all() and torch.isfinite(lse[2]).all()
 
 
+@pytest.mark.parametrize("S", [200, 1536, 1537])
+@pytest.mark.parametrize("b", [1, 40, 140])
+def test_decode_rows_without_a_key(b, S):
+    """Empty prefixes and invalid lengths beside good ones, in caches whose
+    units are never cut and in one where they may be."""
+    lens = [150, 0, 33, 0]
+    q, kv = decode_case(4, 4, 2, b, 64, S, 32, lens, 2, 90 + b)
+    run_decode(q, kv, lens, 2, 32)
+    (kc, ks), (vc, vs) = kv
+    good, lse_good = bd.decode_q8(q.cuda(), cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 2, 32)
+    out, lse = bd.decode_q8(q.cuda(), cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32([150, S + 1, 33, -1]).cuda(), 2, 32)
+    torch.cuda.synchronize()
+    assert bd.device_status() == bd.BD_ERR_DEVICE_TIMEOUT
+    for i in (1, 3):
+        assert torch.isnan(lse[i]).all() and torch.isnan(out[i]).all()
+    for i in (0, 2):
+        assert torch.equal(out[i], good[i]) and torch.equal(lse[i], lse_good[i])
+
+
 def test_decode_wait_that_runs_out_is_reported():
     """One K tile never arrives: the bounded wait runs out, the launch reports
     it, the next one is right."""
