@@ -1,7 +1,7 @@
 // Block decode over a KV cache in 8 bits for few query rows (sm_100a).
 //
 // The mathematics of attn_q8_tc.cuh, for units (a sequence and a kv-head) of
-// at most 16 query rows (32 at d = 32), single tokens above all.  There the
+// at most 16 query rows (32 below d = 128), single tokens above all.  There the
 // 128-row tile of tcgen05 would be almost empty while its softmax still walks 128
 // columns a tile; here a warp takes 8, 16 or 32 rows with mma.sync.m16n8k16, and
 // what a key costs is fetching and converting its 2 d codes.
