@@ -675,8 +675,9 @@ def spec_verify(draft, draft_prob, target_prob, u_accept, u_sample,
     """Accept a prefix of draft [B,b] int32 by speculative sampling and draw
     the token behind it: draft_prob [B,b,V] fp32 (None: the draft was not
     sampled), target_prob [B,b+1,V] fp32, random numbers u_accept [B,b] and
-    u_sample [B] fp32 in [0,1), n_draft [B] int32 (None: b).  Returns
-    (n_accept [B], next_token [B]) int32 on the device."""
+    u_sample [B] fp32 in [0,1), n_draft [B] int32 (None: b).  n_accept or
+    next_token may be n_draft.  Returns (n_accept [B], next_token [B]) int32 on
+    the device."""
     import torch
     B, b = draft.shape
     V = target_prob.shape[-1]

@@ -416,6 +416,13 @@ inline bool aligned4(const void *p)
     return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte; NULL holds none.
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
 // Group sizes of a cache in 8 bits: whole 16-key chunks of a key tile.
 inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
 
@@ -1053,6 +1060,16 @@ bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
         return BD_ERR_INVALID_ARG;
     if (V > bd::kVerifyMaxVocab || B > INT_MAX / bd::kVerifyCluster)
         return BD_ERR_UNSUPPORTED;
+    // A sequence is read by the CTAs of a cluster and written by one of them:
+    // of the inputs, an output may lie only in n_draft's place, entry on entry.
+    const size_t n4 = (size_t)B * 4;
+    if (overlap(n_accept, n4, next_token, n4))
+        return BD_ERR_INVALID_ARG;
+    for (const int32_t *o : {n_accept, next_token})
+        if (overlap(o, n4, draft, n4 * b) || overlap(o, n4, draft_prob, n4 * b * V) ||
+            overlap(o, n4, target_prob, n4 * ((size_t)b + 1) * V) || overlap(o, n4, u_accept, n4 * b) ||
+            overlap(o, n4, u_sample, n4) || (o != n_draft && overlap(o, n4, n_draft, n4)))
+            return BD_ERR_INVALID_ARG;
     bd::VerifyParams p = {draft, draft_prob, target_prob, u_accept, u_sample, n_draft,
                           n_accept, next_token, B, b, V};
     const int segs = (int)cdiv(V, bd::kVerifySeg * bd::kVerifyCluster); // per CTA

@@ -51,11 +51,10 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
-// Accepted positions of sequence i, by one converged warp; -1 for a draft
-// length or a drafted token out of range.
-__device__ __forceinline__ int verify_accept(const VerifyParams &p, int i, int lane)
+// Accepted positions of the nd drafted ones of sequence i, by one converged
+// warp; -1 for a draft length or a drafted token out of range.
+__device__ __forceinline__ int verify_accept(const VerifyParams &p, int i, int nd, int lane)
 {
-    const int nd = p.n_draft ? p.n_draft[i] : p.b;
     if (nd < 0 || nd > p.b)
         return -1;
     int n = nd;
@@ -118,33 +117,28 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(THREADS
 {
     extern __shared__ double seg[]; // sum of each segment's weights
     __shared__ double s_total[2];   // this CTA's, of each pass
-    __shared__ int s_n;
+    __shared__ int s_n, s_nd;
     const int i = blockIdx.x / kVerifyCluster, rank = blockIdx.x % kVerifyCluster;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Either output may lie in n_draft's buffer: every CTA reads its counts here,
+    // once, and nothing is written before a barrier of the cluster is behind.
     if (warp == 0) {
-        const int n = verify_accept(p, i, lane);
+        const int nd = p.n_draft ? p.n_draft[i] : p.b;
+        const int n = verify_accept(p, i, nd, lane);
         if (lane == 0) {
             s_n = n;
-            if (rank == 0) {
-                if (n < 0) {
-                    raise_device_code(DEV_BAD_CACHE_LEN);
-                    p.next_token[i] = -1;
-                }
-                p.n_accept[i] = max(n, 0);
-            }
+            s_nd = nd;
         }
     }
     __syncthreads();
-    const int n = s_n;
-    if (n < 0) // in every CTA of the cluster
-        return;
-    const int nd = p.n_draft ? p.n_draft[i] : p.b;
+    const int n = max(s_n, 0), nd = s_nd;
     const float *pr = p.target_prob + ((size_t)i * (p.b + 1) + n) * p.V;
     const float *qr = n < nd && p.draft_prob ? p.draft_prob + ((size_t)i * p.b + n) * p.V : nullptr;
     const int point = n < nd && !p.draft_prob ? p.draft[(size_t)i * p.b + n] : -1;
     const int v0 = rank * segs * kVerifySeg; // this CTA's entries
     const int v1 = min(p.V, v0 + segs * kVerifySeg);
-    const int mine = v1 > v0 ? (v1 - v0 + kVerifySeg - 1) / kVerifySeg : 0;
+    // (a bad sequence, for every CTA of its cluster, has no entries)
+    const int mine = v1 > v0 && s_n >= 0 ? (v1 - v0 + kVerifySeg - 1) / kVerifySeg : 0;
     bool residual = n < nd;
 
     constexpr int E = kVerifySeg / 32;
@@ -248,8 +242,13 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(THREADS
     const double want = u > 0.0 ? u * total : 0.0; // (a NaN draws the first)
     const double own = s_total[pass];
     const bool here = own > 0.0 && before <= want && (before + own > want || rank == owner_last);
-    if (total <= 0.0 && rank == 0 && threadIdx.x == 0)
-        p.next_token[i] = -1;
+    if (rank == 0 && threadIdx.x == 0) {
+        if (s_n < 0)
+            raise_device_code(DEV_BAD_CACHE_LEN);
+        p.n_accept[i] = max(s_n, 0);
+        if (total <= 0.0)
+            p.next_token[i] = -1;
+    }
     if (warp == 0 && here) {
         // the segment, 32 at a time
         double run = before;

@@ -537,13 +537,16 @@ BD_API bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache,
  *   target_prob  [B, b + 1, V] fp32, DEVICE
  *   u_accept     [B, b] fp32, u_sample [B] fp32, DEVICE, in [0, 1)
  *   n_draft      [B] int32, DEVICE, drafted positions, or NULL: b each
- *   n_accept, next_token  [B] int32, DEVICE (written)
+ *   n_accept, next_token  [B] int32, DEVICE (written); one of them may be
+ *                n_draft, the counts replaced in place.  No other overlap with
+ *                one another or an input
  *
  * A sequence with n_draft[i] outside [0, b] or a drafted token outside [0, V)
  * gets n_accept 0 and next_token -1, and the device status word records
  * BD_ERR_DEVICE_TIMEOUT.  Errors: BD_ERR_INVALID_ARG for a null or misaligned
- * pointer, a size <= 0 or one buffer for both outputs; BD_ERR_UNSUPPORTED for
- * V > 4194304 or B > 268435455; BD_ERR_CUDA if the launch fails.
+ * pointer, a size <= 0 or outputs that overlap one another or an input but
+ * as above; BD_ERR_UNSUPPORTED for V > 4194304 or B > 268435455; BD_ERR_CUDA
+ * if the launch fails.
  */
 BD_API bd_status bd_spec_verify(const int32_t *draft, const float *draft_prob,
                                 const float *target_prob, const float *u_accept,

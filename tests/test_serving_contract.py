@@ -1,0 +1,34 @@
+"""What the header promises of the serving step over a cache in 8 bits at the
+edges of its domain: refusals (host only, nothing is launched) and the
+definitions of oracle/serving.py there."""
+import numpy as np
+import pytest
+
+from oracle import serving
+import block_diffusion_lm_attn_b200 as bd
+from block_diffusion_lm_attn_b200 import build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return bd.load()
+
+
+A = 1 << 20  # fake addresses, 64 KB apart and more; never dereferenced
+VERIFY = dict(draft=A, draft_prob=2 * A, target_prob=3 * A, u_accept=4 * A, u_sample=5 * A, n_draft=6 * A,
+              n_accept=7 * A, next_token=8 * A, B=8, b=4, V=100, stream=None)
+
+
+@pytest.mark.parametrize("out", ["n_accept", "next_token"])
+@pytest.mark.parametrize("at", [A, A + 8 * 4 * 4 - 4, 2 * A, 2 * A + 8 * 4 * 100 * 4 - 4, 3 * A - 28,
+                                3 * A + 8 * 5 * 100 * 4 - 4, 4 * A + 64, 5 * A, 6 * A + 4, 6 * A - 4])
+def test_verify_refuses_outputs_over_inputs(lib, out, at):
+    """The first and last entries of every input, and n_draft's buffer shifted
+    by an entry: another sequence's count."""
+    assert bd.bd_spec_verify(**{**VERIFY, out: at}) == bd.BD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("shift", [-28, -4, 0, 4, 28])
+def test_verify_refuses_outputs_over_one_another(lib, shift):
+    assert bd.bd_spec_verify(**{**VERIFY, "next_token": 7 * A + shift}) == bd.BD_ERR_INVALID_ARG
