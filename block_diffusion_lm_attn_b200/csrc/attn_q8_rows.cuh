@@ -47,7 +47,7 @@ template <int R> struct Qr {
     static constexpr int kMerge = R == 8 ? 8 : 16; // rows merged at a time
     static constexpr int kRing = 0;                // [warp][stage][K, V]
     static constexpr int kO = kRing + kQrWarps * kQrStages * 2 * kQrTile; // [warp][kMerge][pitch] f32
-    static constexpr int kMl = kO + kQrWarps * kMerge * kQrPitch * 4;   // [warp][kMerge] (l, M)
+    static constexpr int kMl = kO + kQrWarps * kMerge * kQrPitch * 4;   // [warp][kMerge] (l, its exponent)
     static constexpr int kBar = kMl + kQrWarps * kMerge * 8;
     static constexpr int kBytes = kBar + 8 * kQrWarps * kQrStages + 16 + 1024;
     static_assert(kBytes <= 227 * 1024, "more shared memory than a CTA may have");
@@ -172,12 +172,12 @@ __global__ void __launch_bounds__(kQrThreads, 1)
             }
     };
     // scales of a 32-key part, two runs of 16 keys; keys that are none take
-    // neutral ones
+    // neutral ones (kQtMidScale: see vmin)
     auto scales = [&](const Seg &s, int k0, float2 *e) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int key = k0 + 16 * c;
-            e[c] = make_float2(1.f, 1.f);
+            e[c] = make_float2(1.f, kQtMidScale);
             if (key < s.hi0) {
                 const size_t at = (size_t)s.kvhead * p.groups + (key >> p.tshift);
                 e[c] = make_float2(p.ks[at], p.vs[at]);
@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(kQrThreads, 1)
         constexpr int NO = kSwap ? NT / 2 : NT;
         float o[MT][NO][4];
         float m[MT][2], l[MT][2];
+        float vmin = kQtMidScale, vmax = kQtMidScale; // V's scales so far
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -284,6 +285,8 @@ __global__ void __launch_bounds__(kQrThreads, 1)
                 if (ks >= sg.hi0)
                     break;
                 const float2 ec[2] = {es[0], es[1]};
+                vmin = fminf(vmin, fminf(ec[0].y, ec[1].y));
+                vmax = fmaxf(vmax, fmaxf(ec[0].y, ec[1].y));
                 // the next part's scales are on their way meanwhile
                 scales(sg, part + 1 < KS / 32 ? ks + 32 : k0 + kQrWarps * KS, es);
                 if constexpr (kSwap) {
@@ -481,6 +484,81 @@ __global__ void __launch_bounds__(kQrThreads, 1)
             ++used;
             fill(sg, i + kQrStages);
         }
+        // V's scales too far apart (kQtSpread): the sums once more, from scores
+        // taken once more, in units of 2^u, u raised to a row's maximum where that
+        // lies kQtLazy above.  (Found out, and summed, as the keys go by, it cost
+        // every call 2 to 10 %.)
+        float u[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            u[mt][0] = m[mt][0];
+            u[mt][1] = m[mt][1];
+        }
+        if (__builtin_expect(vmax > vmin * kQtSpread, 0)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                l[mt][0] = l[mt][1] = 0.f;
+                u[mt][0] = u[mt][1] = -INFINITY;
+            }
+            for (int i = 0; i < kQrStages; ++i)
+                fill(sg, i);
+            for (int i = 0;; ++i) {
+                const int k0 = sg.lo0 + (i * kQrWarps + warp) * KS;
+                if (k0 >= sg.hi0)
+                    break;
+                const int st = used % kQrStages;
+                const uint32_t kb = ring + st * (2 * kQrTile);
+                mbar_wait_warp(bar(st), (uint32_t)((used / kQrStages) & 1), abort_flag);
+                // 8 keys at a time: rows g and g + 8 at keys 2t and 2t + 1, or key g at
+                // rows 2t and 2t + 1 (with 8 keys of zeros behind them)
+#pragma unroll 1
+                for (int ks = k0; ks < min(k0 + KS, sg.hi0); ks += 8) {
+                    uint32_t x[KW];
+                    const int byte = t * (DH / 4);
+                    qr_lds<KW>(kb + qr_place<DH>(ks - k0 + g, byte >> 4) + (byte & 15), x);
+                    const float e = p.ks[(size_t)sg.kvhead * p.groups + (ks >> p.tshift)] * p.pp.scale_log2;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        float s[4] = {};
+#pragma unroll
+                        for (int w = 0; w < KW; ++w) {
+                            const uint32_t lo = half2_of_e4m3x2((uint16_t)x[w]);
+                            const uint32_t hi = half2_of_e4m3x2((uint16_t)(x[w] >> 16));
+                            if constexpr (kSwap) {
+                                const uint32_t a[4] = {lo, 0, hi, 0};
+                                mma_f16(s, a, qf[0][w][0], qf[0][w][1]);
+                            } else {
+                                mma_f16(s, qf[mt][w], lo, hi);
+                            }
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            constexpr int N = kSwap ? 1 : 2; // keys of the row
+                            const float a = fmaxf(e * qs[mt][h], 1.2e-38f);
+                            float y[N], xm = -INFINITY;
+#pragma unroll
+                            for (int n = 0; n < N; ++n) {
+                                y[n] = (ks + (kSwap ? g : 2 * t + n) < seen[mt][h] ? s[N * h + n] : -INFINITY) * a;
+                                xm = fmaxf(xm, y[n]);
+                            }
+#pragma unroll
+                            for (int w = kSwap ? 4 : 1; w < (kSwap ? 32 : 4); w <<= 1)
+                                xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, w));
+                            if (xm > u[mt][h] + kQtLazy) {
+                                l[mt][h] = u[mt][h] == -INFINITY ? l[mt][h] : l[mt][h] * ex2(u[mt][h] - xm);
+                                u[mt][h] = xm;
+                            }
+#pragma unroll
+                            for (int n = 0; n < N; ++n)
+                                l[mt][h] += ex2(y[n] - (u[mt][h] == -INFINITY ? 0.f : u[mt][h]));
+                        }
+                    }
+                }
+                __syncwarp();
+                ++used;
+                fill(sg, i + kQrStages);
+            }
+        }
         // the next segment's first steps are on their way during the merge
         more = src.next(p.pp, nx);
         for (int i = 0; more && i < kQrStages; ++i)
@@ -499,8 +577,15 @@ __global__ void __launch_bounds__(kQrThreads, 1)
                 for (int w = kSwap ? 4 : 1; w < (kSwap ? 32 : 4); w <<= 1)
                     x += __shfl_xor_sync(0xffffffffu, x, w);
                 const int r = warp * S::kMerge + (kSwap ? 2 * t + h : h * 8 + g);
+                float unit = u[mt][h];
+                const float to_unit = qt_normalise(x, unit, m[mt][h]);
                 if (kSwap ? g == 0 : t == 0)
-                    s_ml[r] = make_float2(x, m[mt][h]);
+                    s_ml[r] = make_float2(x, unit);
+#pragma unroll
+                for (int n = 0; n < NO; ++n) {
+                    o[mt][n][kSwap ? h : 2 * h] *= to_unit;
+                    o[mt][n][kSwap ? 2 + h : 2 * h + 1] *= to_unit;
+                }
                 float *dst = s_o + (size_t)r * kQrPitch + (kSwap ? g * (DH / 8) : t * (DH / 4));
                 if constexpr (kSwap) {
 #pragma unroll
@@ -532,7 +617,7 @@ __global__ void __launch_bounds__(kQrThreads, 1)
                 for (int w = 0; w < kQrWarps; ++w) {
                     const float2 ml = s_ml[w * S::kMerge + r];
                     const float f = ml.y == -INFINITY ? 1.f : ex2(ml.y - mx);
-                    ls = fmaf(ml.x, f, ls); // a NaN shows in l whatever M is
+                    ls = fmaf(ml.x, f, ls); // a NaN shows in l whatever its unit is
                     const float4 *x = reinterpret_cast<const float4 *>(s_o + (size_t)(w * S::kMerge + r) * kQrPitch + col);
                     const float4 y0 = x[0], y1 = x[1];
                     acc[0] = fmaf(y0.x, f, acc[0]); acc[1] = fmaf(y0.y, f, acc[1]);

@@ -6,7 +6,10 @@
 //     x_j   = log2(e) / sqrt(d) * s_K(j) 2^e (hi + lo) . c_K(j)
 //     P_j   = 2^(x_j + log2 s_V(j) - M),  O = sum_j P_j c_V(j),
 //     l     = sum_j P_j / s_V(j),         out = O / l,  lse = ln 2 (M + log2 l)
-// for any M; M follows max_j (x_j + log2 s_V(j)), so that P fits 11 bits.
+// for any M; M follows max_j (x_j + log2 s_V(j)), so that P fits 11 bits.  Where
+// V's scales lie so far apart that a P beside M could be 0 in fp32 although its
+// key has weight (kQtSpread), l is summed from 2^(x_j - U) instead, U following
+// max_j x_j: more than one exponential a score, in a tile that no model has.
 // A query row q = 2^e (hi + lo) is split into two e4m3 halves: hi rounds 2^-e q
 // to 4 significant bits, lo rounds the rest to 4 more, which a bf16 has.  S =
 // Q K^T is then two kind::f8f6f4 products straight on the codes in shared
@@ -63,8 +66,8 @@ constexpr int kQtSmemK = kQtSmemQ + 2 * kQtTile;
 constexpr int kQtSmemV = kQtSmemK + kQtKStages * kQtTile;
 constexpr int kQtSmemW = kQtSmemV + kQtVStages * kQtTile; // V in f16: 2 buffers
 constexpr int kQtSmemSc = kQtSmemW + 2 * kTileBytes; // 8 tiles: 8 scales of K, 8 of V
-constexpr int kQtSmemL = kQtSmemSc + 8 * 64;         // (l, M) [2][2][128]
-constexpr int kQtSmemQs = kQtSmemL + 4 * kTcM * 8;        // row scales of Q [2][128]
+constexpr int kQtSmemL = kQtSmemSc + 8 * 64;         // (l, u, 2^(M - u)) [2][2][128]
+constexpr int kQtSmemQs = kQtSmemL + 4 * kTcM * 16;       // row scales of Q [2][128]
 constexpr int kQtSmemSeg = kQtSmemQs + 2 * kTcM * 4;      // 4 segments, 128 B each
 constexpr int kQtSmemBar = kQtSmemSeg + 4 * 128;
 constexpr int kQtSmemBytes = kQtSmemBar + 512 + 1024; // + alignment slack
@@ -290,6 +293,30 @@ __device__ __forceinline__ float lg2(float x)
 // heads of large scores took 1.3 us a tile where others took 1.1.
 constexpr float kQtTop = 3.f, kQtLazy = 12.f;
 
+// l may be summed from P as long as no weight of consequence is 0 in P.  With
+// V's scales 2^w apart at most, x the score (in log2) of a key and X the row's
+// largest, its P is 2^(x - X - w + kQtTop) or more: above fp32's 2^-126, at w =
+// 72, for weights from 2^-57 of the largest on.  A raise of M by more than 126,
+// which takes the sum before it to 0, asks for scores 126 - w - kQtLazy = 42
+// apart.  Both bounds hold what 2^30 keys can lose below 2^-12.  Counting from
+// 2^-8 keeps 1 / s_V, and with it l over 2^30 keys, in range too: V's scales
+// from 2^-80 to 2^64 take the sum from P if they lie no further apart.
+constexpr float kQtSpread = 4722366482869645213696.f; // 2^72
+constexpr float kQtMidScale = 1.f / 256;
+
+// A finished run's sum of weights, l 2^u, as l in [1, 2) (0 without a visible
+// key, NaN stays) and an exponent u that a float holds; returns what O, in units
+// of 2^m, is multiplied by to be in units of 2^u.
+__device__ __forceinline__ float qt_normalise(float &l, float &u, float m)
+{
+    const bool some = l > 0.f && l < INFINITY;
+    const int k = some ? min((int)(__float_as_uint(l) >> 23) - 127, 126) : 0;
+    const float f = some ? ex2(m - u - (float)k) : 1.f;
+    l *= exp2_int(-k);
+    u += (float)k;
+    return f;
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
@@ -425,7 +452,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + kQtSmemBar + 272);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sbase + kQtSmemBar + 280);
     Seg *seg_ring = reinterpret_cast<Seg *>(sbase + kQtSmemSeg); // nt = 0: no more
-    float2 *s_l = reinterpret_cast<float2 *>(sbase + kQtSmemL);
+    float4 *s_l = reinterpret_cast<float4 *>(sbase + kQtSmemL);
     float *s_qs = reinterpret_cast<float *>(sbase + kQtSmemQs);
     const float *s_sc = reinterpret_cast<const float *>(sbase + kQtSmemSc);
 
@@ -763,6 +790,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const int seen = min(hi, sg.len + (p.pp.mode == 0 ? p.pp.b : p.pp.mode == 1 ? jr + 1 : 0));
             const bool live = wrow < nrows; // a warp without rows only arrives
             float m = -INFINITY, l = 0.f; // running maximum (raised lazily), sum
+            float vmin = kQtMidScale, vmax = kQtMidScale; // V's scales so far
+            float u = INFINITY; // finite once they lie far apart: l is in units of 2^u, not 2^m
             for (int i = (j0 ^ wg) & 1; i < n; i += 2) {
                 const int j = j0 + i; // tile
                 if (!(ok = wait(bar_sfull(wg), (uint32_t)((j >> 1) & 1))))
@@ -803,7 +832,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     for (int c = 0; c < NG; ++c) {
                         const bool in = ks + c * (kTcN / NG) < hi;
                         ea[c] = fmaxf(sc[c] * qs, 1.2e-38f);
-                        ev[c] = in ? sc[8 + c] : 1.f;
+                        ev[c] = in ? sc[8 + c] : kQtMidScale;
+                        vmin = fminf(vmin, ev[c]);
+                        vmax = fmaxf(vmax, ev[c]);
                         const float *x = s + c * (kTcN / NG);
                         float mc[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
 #pragma unroll
@@ -817,11 +848,27 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         break;
                     tc_fence_after();
                     const bool need = mt > m + (kQtTop + kQtLazy);
-                    if (__any_sync(0xffffffffu, need)) {
+                    const bool wide = vmax > vmin * kQtSpread; // and so from here on
+                    if (__any_sync(0xffffffffu, need || wide)) {
+                        if (__builtin_expect(wide, 0)) { // the sum apart
+                            float xm = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < kTcN; ++c)
+                                xm = fmaxf(xm, s[c] * ea[c / (kTcN / NG)]);
+                            u = u < INFINITY ? u : m;
+                            if (xm > u + kQtLazy) {
+                                l = u == -INFINITY ? l : l * ex2(u - xm);
+                                u = xm;
+                            }
+                            const float nu = u == -INFINITY ? 0.f : -u;
+#pragma unroll
+                            for (int c = 0; c < kTcN; ++c)
+                                l += ex2(fmaf(s[c], ea[c / (kTcN / NG)], nu));
+                        }
                         float c = 1.f;
                         if (need) {
                             c = m == -INFINITY ? 0.f : ex2(m - (mt - kQtTop));
-                            l = m == -INFINITY ? l : l * c; // 0, or NaN for good
+                            l = m == -INFINITY || wide ? l : l * c; // 0, or NaN for good
                             m = mt - kQtTop;
                         }
                         // the TMEM read-modify-write of O is warp-collective
@@ -863,7 +910,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         }
                         if (W == 16)
                             tmem_st8(tp + c * 8, pk);
-                        l = fmaf((r0 + r1) + (r2 + r3), 1.f / ev[c], l);
+                        l = fmaf((r0 + r1) + (r2 + r3), wide ? 0.f : 1.f / ev[c], l);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -886,7 +933,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             if ((jl & 1) != wg &&
                 (!(ok = wait(bar_sfull(jl & 1), (uint32_t)((jl >> 1) & 1))) || !(ok = split(si + 1))))
                 break;
-            s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float2(l, m);
+            u = u < INFINITY ? u : m;
+            const float to_u = qt_normalise(l, u, m);
+            s_l[((si & 1) * 2 + wg) * kTcM + row] = make_float4(l, u, to_u, 0.f);
             mbar_arrive(bar_l);
             // The last PV.  (The phase before on that barrier, PV_{jl-2}, was
             // waited for by the warpgroup of tile jl before it arrived here.)
@@ -894,16 +943,16 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 !(ok = wait(bar_odone(jl & 1), (uint32_t)((jl >> 1) & 1))))
                 break;
             tc_fence_after();
-            // factors of the two O to the common maximum; with one tile, one O
+            // factors of the two O to the common exponent; with one tile, one O
             // is unwritten
-            const float2 l0 = s_l[(si & 1) * 2 * kTcM + row], l1 = s_l[((si & 1) * 2 + 1) * kTcM + row];
+            const float4 l0 = s_l[(si & 1) * 2 * kTcM + row], l1 = s_l[((si & 1) * 2 + 1) * kTcM + row];
             const bool use0 = n > 1 || (j0 & 1) == 0, use1 = n > 1 || (j0 & 1) == 1;
             const float mx = fmaxf(l0.y, l1.y);
             const float f0 = l0.y == -INFINITY ? 1.f : ex2(l0.y - mx);
             const float f1 = l1.y == -INFINITY ? 1.f : ex2(l1.y - mx);
-            const float ls = l0.x * f0 + l1.x * f1; // a NaN shows in l whatever m is
+            const float ls = l0.x * f0 + l1.x * f1; // a NaN shows in l whatever u is
             const float inv = ls == 0.f ? 0.f : 1.f / ls;
-            const float w0 = f0 * inv, w1 = f1 * inv;
+            const float w0 = l0.z * (f0 * inv), w1 = l1.z * (f1 * inv);
             const bool valid = row < nrows;
             const size_t grow = (size_t)sg.out_row0 + row;
             const size_t prow = ((size_t)blockIdx.x * 2 + sg.slot) * kTcM + row;

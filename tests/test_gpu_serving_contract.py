@@ -8,7 +8,7 @@ import torch
 from oracle import serving
 import block_diffusion_lm_attn_b200 as bd
 from block_diffusion_lm_attn_b200 import build
-from test_gpu_serving import i32, verify_case
+from test_gpu_serving import gen, i32, randn, run_decode, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,59 @@ def test_verify_replaces_the_counts_in_place(B, point, out):
         assert counts.data_ptr() in (n.data_ptr(), t.data_ptr())
         assert list(zip(n.tolist(), t.tolist())) == want
     assert bd.device_status() == bd.BD_OK
+
+
+# ----------------------------------------------------------------------------
+# decode
+
+# (B, Hq, Hkv, b): 4 and 28 rows a unit on the kernel for few rows (28 below d =
+# 128 alone), 80 on the 128-row tiles
+ROWS = [(4, 1, 1), (8, 2, 7), (4, 2, 40)]
+
+
+def far_scales(g, H, S, d, group, lo, hi):
+    """A cache of one sequence: random keys, value codes between 1 and 448 in
+    size, and V scales of any power of two from 2^lo to 2^hi."""
+    kc = torch.randint(0x30, 0x48, (1, H, S, d), generator=g).to(torch.uint8)
+    vc = torch.randint(0x38, 0x7f, (1, H, S, d), generator=g).to(torch.uint8)
+    kc, vc = ((c | (torch.randint(0, 2, c.shape, generator=g) * 128).to(torch.uint8)) for c in (kc, vc))
+    n = -(-S // group)
+    return (kc, torch.ones(1, H, n)), (vc, torch.exp2(torch.randint(lo, hi + 1, (1, H, n), generator=g).float()))
+
+
+@pytest.mark.parametrize("Hq,H,b", ROWS)
+@pytest.mark.parametrize("scales", [(-100, 30), (30, -100), (-64, 90), (120, -80), (-100, -100), (120, 120)])
+def test_decode_two_keys_whose_value_scales_lie_far_apart(Hq, H, b, scales):
+    """Equal scores: half the weight each, whatever their V scales; the two in
+    one tile, and in tiles of different warps and warpgroups.  (A scale's
+    logarithm is off by 2^-22 of it, 120 at most, and counts in both keys.)"""
+    d, group = 64, 32
+    for at in (16, 40, 100, 150, 500):
+        S, lens = 704, [at + 1]
+        vc = torch.full((1, H, S, d), 0x38, dtype=torch.uint8)
+        kc = torch.zeros((1, H, S, d), dtype=torch.uint8)
+        kc[:, :, 1:at] = 0xfe  # -448: no weight beside 0
+        q = torch.ones((1, Hq, b, d), dtype=torch.bfloat16)
+        vs = torch.full((1, H, S // group), scales[0], dtype=torch.float32)
+        vs[:, :, at // group:] = scales[1]
+        kv = (kc, torch.ones(1, H, S // group)), (vc, torch.exp2(vs))
+        out, lse = run_decode(q, kv, lens, 2, group)
+        assert (lse.cpu() - np.log(2.0)).abs().max() <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("Hq,H,b", ROWS)
+@pytest.mark.parametrize("d,group", [(128, 16), (128, 64), (64, 32), (32, 128)])
+@pytest.mark.parametrize("lo,hi,size", [(-64, 20, 1.0), (-100, 110, 1.0), (-100, 110, 30.0), (60, 110, 1.0)])
+def test_decode_value_scales_of_any_size(Hq, H, b, d, group, lo, hi, size):
+    """Random scales of V, scores close together and far apart, in whole units
+    and cut ones."""
+    g = gen(d + group + hi)
+    lens = [900]
+    kv = far_scales(g, H, 1024, d, group, lo, hi)
+    q = randn(g, 1, Hq, b, d, scale=size)
+    for grid in (0, 3):
+        assert bd.bd_attn_debug_set_grid(grid) == bd.BD_OK
+        try:
+            run_decode(q, kv, lens, 1, group)
+        finally:
+            bd.bd_attn_debug_set_grid(0)
