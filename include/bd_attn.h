@@ -374,6 +374,7 @@ BD_API size_t bd_sprint_workspace_bytes(int B, int S_cap);
  *   k_scale, v_scale  [B, Hkv, ceil(S_cap / group)] fp32: one scale for every
  *                     `group` consecutive positions of a kv-head; a position's
  *                     values are its codes times its group's scale
+ *                     (an infinity where fp32 does not hold the product)
  *   group             16, 32, 64 or 128
  * bd_cache_append_q8 writes powers of two between 2^-64 and 2^120 as scales.
  * The reading calls take any scale from 2^-100 to 2^120 in the groups that
@@ -452,7 +453,8 @@ BD_API bd_status bd_rope(const void *q, const void *k, void *q_out, void *k_out,
  * 2^max(-64, k), k the smallest with |x| <= 448 * 2^k over the finite values
  * of the rows that it then holds (the new ones, and those below cache_len[i]),
  * and all of those rows the codes rne(x / s): +-inf becomes +-448, NaN stays
- * NaN.  Rows that stay are requantised from their values, which is exact
+ * NaN.  At the largest scale, 2^120, codes are at most +-240: 256 2^120 would be
+ * an infinity in fp32 and bf16.  Rows that stay are requantised from their values, which is exact
  * unless they fall below the smallest code, 2^-9 s.  Positions from
  * cache_len[i]+n_new[i] on keep their codes, and groups that take no row keep
  * their scales; positions behind the rows in a written group lose their value.

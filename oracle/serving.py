@@ -72,10 +72,10 @@ _TABLE = e4m3_table()
 _POSITIVE = _TABLE[:127]  # increasing: 0 .. 448
 
 
-def e4m3_encode(x) -> np.ndarray:
-    """Nearest code, ties to the even code, +-448 beyond the range."""
+def e4m3_encode(x, top=448.0) -> np.ndarray:
+    """Nearest code, ties to the even code, +-top (a code) beyond it."""
     x = np.asarray(x, dtype=np.float64)
-    a = np.minimum(np.abs(np.where(np.isnan(x), 0.0, x)), 448.0)
+    a = np.minimum(np.abs(np.where(np.isnan(x), 0.0, x)), top)
     hi = np.clip(np.searchsorted(_POSITIVE, a), 1, 126)
     lo = hi - 1
     down, up = a - _POSITIVE[lo], _POSITIVE[hi] - a
@@ -102,7 +102,8 @@ def group_scale(values) -> float:
 
 def append_q8(codes, scale, cache_len, new, n_new, group):
     """codes uint8 [B, H, S, d], scale [B, H, groups], new [B, H, b, d] float64.
-    Returns the codes and scales afterwards."""
+    Returns the codes and scales afterwards.  At the scale 2^120 codes are at
+    most 240: the next one stands for 2^128, beyond fp32 and bf16."""
     codes, scale = codes.copy(), np.array(scale, dtype=np.float64)
     B, H, S, d = codes.shape
     for i in range(B):
@@ -116,7 +117,7 @@ def append_q8(codes, scale, cache_len, new, n_new, group):
                         for p in range(p0, p1)]
                 s = group_scale(rows)
                 for p, r in zip(range(p0, p1), rows):
-                    codes[i, h, p] = e4m3_encode(r / s)
+                    codes[i, h, p] = e4m3_encode(r / s, 240.0 if s == 2.0 ** 120 else 448.0)
                 scale[i, h, g] = s
     return codes, scale
 

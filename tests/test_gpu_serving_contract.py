@@ -8,7 +8,7 @@ import torch
 from oracle import serving
 import block_diffusion_lm_attn_b200 as bd
 from block_diffusion_lm_attn_b200 import build
-from test_gpu_serving import gen, i32, randn, run_decode, verify_case
+from test_gpu_serving import bits, f64, gen, i32, ok, randn, run_decode, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -52,6 +52,40 @@ def test_verify_replaces_the_counts_in_place(B, point, out):
         assert counts.data_ptr() in (n.data_ptr(), t.data_ptr())
         assert list(zip(n.tolist(), t.tolist())) == want
     assert bd.device_status() == bd.BD_OK
+
+
+# ----------------------------------------------------------------------------
+# the cache
+
+
+@pytest.mark.parametrize("d,group", [(128, 64), (32, 16)])
+def test_append_and_read_back_of_the_largest_values(d, group):
+    """The largest bf16, infinities and NaN: finite values read back finite,
+    and stay when rows join their group."""
+    B, H, S, b = 1, 2, 2 * group, 9
+    g = gen(d)
+    new = randn(g, B, H, b, d)
+    top = torch.finfo(torch.bfloat16).max
+    new[0, :, 2, ::3], new[0, :, 3, 1::3] = top, -top
+    new[0, 0, 4, :3] = torch.tensor([float("inf"), float("-inf"), float("nan")])
+    dev = [torch.zeros((B, H, S, d), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in (0, 1)]
+    dev += [torch.ones((B, H, S // group), device="cuda") for _ in (0, 1)]
+    cl = i32([0]).cuda()
+    rc, rs = np.zeros((B, H, S, d), np.uint8), np.ones((B, H, S // group))
+    for lens, rows in (([0], new), ([b], randn(g, B, H, 3, d))):
+        bd.cache_append_q8(*dev, cl, rows.cuda(), rows.cuda(), group)
+        ok()
+        rc, rs = serving.append_q8(rc, rs, lens, f64(rows), [rows.shape[2]], group)
+        for c, s in ((dev[0], dev[2]), (dev[1], dev[3])):
+            got = bits(c)
+            assert ((got == rc) | (((got & 127) == 127) & ((rc & 127) == 127))).all()
+            np.testing.assert_array_equal(f64(s), rs)
+        ko, vo = bd.cache_read_q8(*dev, cl, group)
+        ok()
+        want = serving.values(rc, rs, group)
+        for o in (ko, vo):
+            np.testing.assert_array_equal(f64(o)[:, :, :int(cl[0])], want[:, :, :int(cl[0])])
+            assert torch.isfinite(o[0, :, 2:4]).all() and torch.isnan(o).sum() == 1
 
 
 # ----------------------------------------------------------------------------

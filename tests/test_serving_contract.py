@@ -32,3 +32,20 @@ def test_verify_refuses_outputs_over_inputs(lib, out, at):
 @pytest.mark.parametrize("shift", [-28, -4, 0, 4, 28])
 def test_verify_refuses_outputs_over_one_another(lib, shift):
     assert bd.bd_spec_verify(**{**VERIFY, "next_token": 7 * A + shift}) == bd.BD_ERR_INVALID_ARG
+
+
+# ----------------------------------------------------------------------------
+# the cache
+
+
+def test_append_keeps_the_largest_values_finite():
+    """255 2^120, the largest bf16, would round to the code of 2^128."""
+    big = 255.0 * 2.0 ** 120
+    new = np.array([big, -big, 1.0, 248.0 * 2.0 ** 120, np.inf, -np.inf, np.nan]).reshape(1, 1, 7, 1)
+    c, s = serving.append_q8(np.zeros((1, 1, 16, 1), np.uint8), np.ones((1, 1, 1)), [0], new, [7], 16)
+    assert s[0, 0, 0] == 2.0 ** 120
+    v = serving.values(c, s, 16).ravel()[:7] / 2.0 ** 120
+    assert v[:6].tolist() == [240.0, -240.0, 0.0, 240.0, 240.0, -240.0] and np.isnan(v[6])
+    # kept beside a smaller row, they stay
+    c2, s2 = serving.append_q8(c, s, [7], np.ones((1, 1, 1, 1)), [1], 16)
+    assert s2[0, 0, 0] == 2.0 ** 120 and (c2[0, 0, :7] == c[0, 0, :7]).all()
