@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kQrThreads, 1)
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const unsigned all = __ballot_sync(0xffffffffu, finite);
                 finite = ((all >> (lane & ~3)) & 15u) == 15u;
-                const int k = max(q8_scale_exp(finite ? amax : 0.f), -100);
+                const int k = q8_scale_exp(finite ? amax : 0.f, kQtMinQExp);
                 const float inv = finite ? exp2_int(-k) : NAN;
                 qs[mt][h] = exp2_int(k);
 #pragma unroll

@@ -351,6 +351,11 @@ __device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b)
     return r;
 }
 
+// The smallest exponent of a query row's scale: 2^k and 2^-k stay normal.  A row of
+// the smallest normal values, 2^-126, is then still split from 1 on, and with K's
+// largest scale has scores that count.
+constexpr int kQtMinQExp = -126;
+
 // A query row (thread = row) as two halves of e4m3 codes, hi and lo, in the
 // 128-byte swizzle of 128-byte rows at `dst` and `dst` + kQtTile; returns the
 // row's scale.
@@ -369,8 +374,8 @@ __device__ __forceinline__ float qt_split_row(const bf16 *src, bool valid, uint3
     }
     const float amax = fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
     const bool finite = (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
-    // 2^-k q reaches 448 at most; k stays where 2^k and 2^-k are normal
-    const int k = max(q8_scale_exp(finite ? amax : 0.f), -100);
+    // 2^-k q reaches 448 at most
+    const int k = q8_scale_exp(finite ? amax : 0.f, kQtMinQExp);
     const float inv = finite ? exp2_int(-k) : NAN;
 #pragma unroll
     for (int c = 0; c < DH / 16; ++c) { // 16 codes of each half

@@ -90,14 +90,14 @@ __device__ __forceinline__ float2 float2_of_e4m3x2(uint16_t c)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// k of the smallest power of two with amax <= 448 * 2^k, -64 or more.  448 =
+// k of the smallest power of two with amax <= 448 * 2^k, `least` or more.  448 =
 // 1.75 * 2^8: a mantissa above 1.75 takes the next exponent.  amax is finite.
-__device__ __forceinline__ int q8_scale_exp(float amax)
+__device__ __forceinline__ int q8_scale_exp(float amax, int least)
 {
     const uint32_t u = __float_as_uint(amax);
     const int e = (int)(u >> 23) - 127;
     const int k = e - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return max(k, kQ8MinExp);
+    return max(k, least);
 }
 __device__ __forceinline__ float exp2_int(int k) // -126 <= k <= 127
 {
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kQ8Threads, 4)
     amax = red[0];
     for (int x = 1; x < (int)blockDim.x / 32; ++x)
         amax = fmaxf(amax, red[x]);
-    const int k = q8_scale_exp(amax);
+    const int k = q8_scale_exp(amax, kQ8MinExp);
     const float s = exp2_int(k), inv = exp2_int(-k);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {

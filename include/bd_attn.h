@@ -506,7 +506,8 @@ BD_API bd_status bd_cache_read_q8(const void *k_cache, const void *v_cache,
  * advance = 0).  Codes of positions that no row of the block sees are not
  * used, NaN codes among them; in mode 1 a NaN value in one of the block's own
  * V rows reaches every row of the block.  A query row with an infinity or a
- * NaN gives NaN.
+ * NaN gives NaN.  Queries may be as small as bf16's smallest normal value; the
+ * largest |q| |k| / sqrt(d) of a row has to fit fp32.
  *
  * Errors: as bd_attn_decode and, for the cache, bd_cache_append_q8.
  */

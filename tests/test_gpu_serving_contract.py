@@ -142,3 +142,15 @@ def test_decode_value_scales_of_any_size(Hq, H, b, d, group, lo, hi, size):
             run_decode(q, kv, lens, 1, group)
         finally:
             bd.bd_attn_debug_set_grid(0)
+
+
+@pytest.mark.parametrize("Hq,H,b", ROWS)
+@pytest.mark.parametrize("d,qe,ke", [(128, -80, 80), (64, -100, 98), (128, -125, 118), (32, -60, 60)])
+def test_decode_small_queries_over_large_keys(Hq, H, b, d, qe, ke):
+    """Query rows of 2^qe, keys of 2^ke: scores of order one and more."""
+    lens = [300]
+    g = gen(d - qe)
+    (kc, ks), v = far_scales(g, H, 400, d, 32, -3, 0)
+    q = (randn(g, 1, Hq, b, d).float().clamp(-3, 3) * 2.0 ** qe).to(torch.bfloat16)
+    q[:, 0] = (q[:, 0].float() * 2.0 ** -4).to(torch.bfloat16) if qe > -120 else q[:, 0]
+    run_decode(q, ((kc, ks * 2.0 ** ke), v), lens, 0, 32)
