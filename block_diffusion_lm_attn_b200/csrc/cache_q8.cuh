@@ -6,10 +6,11 @@
 // The writer gives a group the smallest power of two s = 2^k >= 2^-64 with
 // amax <= 448 s over the rows that it then holds (448: the largest e4m3), and
 // codes rne(x / s).  With a power of two, x / s is exact, c s is exact in
-// bf16, and rows that stay in a partly filled group are requantised without a
-// second rounding unless they fall below the smallest code: c' = c s / s'.
-// Nothing of an older, larger scale remains: rows of a rejected draft stop
-// costing precision with the next write.
+// bf16, and rows that stay in a partly filled group are requantised, c' = rne(c s /
+// s'), without a second rounding from 2^-6 s' on, where codes have their three
+// bits; below, to a multiple of 2^-9 s'.  The scale falls again with the next write
+// behind a rejected draft's large rows, the bits that they cost the prefix do not
+// come back.
 //
 // Bound by HBM: 2 bytes read and 1 written per value on the way in, the
 // reverse on the way back; the rows that share the first written group are

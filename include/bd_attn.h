@@ -454,8 +454,12 @@ BD_API bd_status bd_rope(const void *q, const void *k, void *q_out, void *k_out,
  * of the rows that it then holds (the new ones, and those below cache_len[i]),
  * and all of those rows the codes rne(x / s): +-inf becomes +-448, NaN stays
  * NaN.  At the largest scale, 2^120, codes are at most +-240: 256 2^120 would be
- * an infinity in fp32 and bf16.  Rows that stay are requantised from their values, which is exact
- * unless they fall below the smallest code, 2^-9 s.  Positions from
+ * an infinity in fp32 and bf16.
+ * Rows that stay are requantised from the values that they have.  Where the old
+ * scale is one that this call wrote, that is exact for values of 2^-6 s and more
+ * (and for 0); smaller ones are rounded to a multiple of 2^-9 s.  What is lost
+ * stays lost: a large row costs the rows before it in its group precision for
+ * good, also as a draft that the next write replaces.  Positions from
  * cache_len[i]+n_new[i] on keep their codes, and groups that take no row keep
  * their scales; positions behind the rows in a written group lose their value.
  *

@@ -88,6 +88,35 @@ def test_append_and_read_back_of_the_largest_values(d, group):
             assert torch.isfinite(o[0, :, 2:4]).all() and torch.isnan(o).sum() == 1
 
 
+@pytest.mark.parametrize("d,group", [(128, 64), (64, 16), (32, 128)])
+def test_append_rounds_kept_values_below_the_normal_codes(d, group):
+    """Every code kept at scale 1, a row that asks for 2 to 2^11, then a small
+    one in its place: kept values are exact from 2^-6 of the scale on, and what
+    is rounded below stays so."""
+    B, H, S = 1, 2, 2 * group
+    n = group - 2
+    kc = torch.arange(n * d).reshape(1, 1, n, d) % 256
+    kc = torch.where((kc & 127) == 127, 9, kc).to(torch.uint8).expand(B, H, n, d)
+    codes = torch.zeros((B, H, S, d), dtype=torch.uint8)
+    codes[:, :, :n] = kc
+    for k in (1, 2, 5, 11):
+        dev = [codes.cuda().view(torch.float8_e4m3fn) for _ in (0, 1)]
+        dev += [torch.ones((B, H, S // group), device="cuda") for _ in (0, 1)]
+        cl = i32([n]).cuda()
+        rc, rs = codes.numpy(), np.ones((B, H, S // group))
+        for top in (448.0 * 2.0 ** k, 0.5):
+            row = torch.full((B, H, 1, d), top, dtype=torch.bfloat16)
+            bd.cache_append_q8(*dev, cl, row.cuda(), row.cuda(), group, advance=False)
+            ok()
+            rc, rs = serving.append_q8(rc, rs, [n], f64(row), [1], group)
+            for c, s in ((dev[0], dev[2]), (dev[1], dev[3])):
+                np.testing.assert_array_equal(bits(c)[:, :, :n + 1], rc[:, :, :n + 1])
+                np.testing.assert_array_equal(f64(s), rs)
+        was, now = (serving.values(x, y, group)[:, :, :n] for x, y in ((codes.numpy(), np.ones_like(rs)), (rc, rs)))
+        large = np.abs(was) >= 2.0 ** (k - 6)
+        assert (was[large] == now[large]).all() and (was != now).any()
+
+
 # ----------------------------------------------------------------------------
 # decode
 

@@ -49,3 +49,32 @@ def test_append_keeps_the_largest_values_finite():
     # kept beside a smaller row, they stay
     c2, s2 = serving.append_q8(c, s, [7], np.ones((1, 1, 1, 1)), [1], 16)
     assert s2[0, 0, 0] == 2.0 ** 120 and (c2[0, 0, :7] == c[0, 0, :7]).all()
+
+
+def test_append_rounds_kept_values_below_the_normal_codes():
+    """Scale 1, kept values of 2^-6 to 2^-9; a row of 896 doubles the scale, a
+    small draft in its place brings a small one back, but not the bits."""
+    kept = np.array([9, 15, 8, 16, 17, 1]) * 2.0 ** -9
+    codes = serving.e4m3_encode(np.append(kept, [0.0, 0.0])).reshape(1, 1, 8, 1)
+    assert codes.ravel()[:6].tolist() == [0x09, 0x0f, 0x08, 0x10, 0x10, 0x01]
+    kept[4] = 16 * 2.0 ** -9  # 17 has five bits
+    c, s = serving.append_q8(codes, np.ones((1, 1, 1)), [6], np.full((1, 1, 1, 1), 896.0), [1], 8)
+    assert s[0, 0, 0] == 2.0
+    lost = np.array([8, 16, 8, 16, 16, 0]) * 2.0 ** -9  # multiples of 2^-9 2, ties to even
+    assert serving.values(c, s, 8).ravel()[:6].tolist() == lost.tolist()
+    c, s = serving.append_q8(c, s, [6], np.full((1, 1, 1, 1), 0.5), [1], 8)
+    assert s[0, 0, 0] == 2.0 ** -9
+    assert serving.values(c, s, 8).ravel()[:6].tolist() == lost.tolist()
+
+
+def test_append_keeps_values_of_normal_codes_exactly():
+    """From 2^-6 of the new scale on every kept value survives any scale."""
+    table = serving.e4m3_table()
+    codes = np.arange(256, dtype=np.uint8)[np.isfinite(table)].reshape(1, 1, 254, 1)
+    codes = np.concatenate([codes, np.zeros((1, 1, 2, 1), np.uint8)], 2)
+    for k in range(12):
+        c, s = serving.append_q8(codes, np.ones((1, 1, 1)), [254], np.full((1, 1, 1, 1), 448.0 * 2.0 ** k), [1], 256)
+        assert s[0, 0, 0] == 2.0 ** k
+        x, y = table[codes.ravel()[:254]], serving.values(c, s, 256).ravel()[:254]
+        large = np.abs(x) >= 2.0 ** (k - 6)
+        assert (x[large] == y[large]).all() and (np.abs(x - y) <= 2.0 ** (k - 10)).all()
