@@ -338,6 +338,9 @@ bd_status decode_validate(const void *q_blk, const void *k_cache,
     if ((long long)B * Hkv > 65535LL || pl.row_tiles > 65535 ||
         (long long)B * Hkv * pl.row_tiles > (1LL << 30))
         return BD_ERR_UNSUPPORTED;
+    // rows of the output are counted in 32 bits
+    if (pl.rows_all > (size_t)INT_MAX)
+        return BD_ERR_UNSUPPORTED;
     return BD_OK;
 }
 

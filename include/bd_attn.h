@@ -189,8 +189,8 @@ BD_API size_t bd_attn_bwd_workspace_bytes(int B, int Hq, int L);
  * Errors: BD_ERR_INVALID_ARG for a null or misaligned pointer, any size <= 0,
  * Hq % Hkv != 0, S_cap < b in modes 0 and 1, intra_block_mode not 0/1/2, or
  * a workspace smaller than required; BD_ERR_UNSUPPORTED for d not in {32,
- * 64, 128}; BD_ERR_CUDA if the launch (or the internal workspace allocation)
- * fails.  A cache_len[i] outside [0, S_cap - b] (modes 0 and 1) or [0, S_cap]
+ * 64, 128}, B Hkv > 65535 or B Hq b > 2^31 - 1; BD_ERR_CUDA if the launch (or
+ * the internal workspace allocation) fails.  A cache_len[i] outside [0, S_cap - b] (modes 0 and 1) or [0, S_cap]
  * (mode 2) is caught on the device: that sequence's rows are written as NaN
  * with lse NaN, and the device status word (see bd_attn_get_device_status)
  * records BD_ERR_DEVICE_TIMEOUT.

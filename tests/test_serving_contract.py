@@ -78,3 +78,15 @@ def test_append_keeps_values_of_normal_codes_exactly():
         x, y = table[codes.ravel()[:254]], serving.values(c, s, 256).ravel()[:254]
         large = np.abs(x) >= 2.0 ** (k - 6)
         assert (x[large] == y[large]).all() and (np.abs(x - y) <= 2.0 ** (k - 10)).all()
+
+
+# ----------------------------------------------------------------------------
+# decode
+
+
+def test_decode_refuses_more_rows_than_32_bits_count(lib):
+    """2^32 query rows in units of a size that is allowed."""
+    big = dict(q_blk=A, k_cache=2 * A, v_cache=3 * A, cache_len=6 * A, out=7 * A, lse=8 * A, B=512, Hq=64, Hkv=1,
+               b=131000, d=32, intra_block_mode=0, stream=None, S_cap=1 << 18, workspace=9 * A, workspace_bytes=1 << 30)
+    assert bd.bd_attn_decode_q8(**big, k_scale=4 * A, v_scale=5 * A, group=32) == bd.BD_ERR_UNSUPPORTED
+    assert bd.bd_attn_decode(**big) == bd.BD_ERR_UNSUPPORTED
