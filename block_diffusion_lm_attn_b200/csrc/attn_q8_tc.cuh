@@ -11,8 +11,10 @@
 // key has weight (kQtSpread), l is summed from 2^(x_j - U) instead, U following
 // max_j x_j: more than one exponential a score, in a tile that no model has.
 // A query row q = 2^e (hi + lo) is split into two e4m3 halves: hi rounds 2^-e q
-// to 4 significant bits, lo rounds the rest to 4 more, which a bf16 has.  S =
-// Q K^T is then two kind::f8f6f4 products straight on the codes in shared
+// to 4 significant bits, lo rounds the rest to 4 more, together the 8 of a bf16
+// for values from 2^-10 of the row's largest on; smaller ones are off by at most
+// 2^-17 of the largest, where codes end.  (The kernel for few rows takes queries
+// in f16, which holds these too.)  S = Q K^T is then two kind::f8f6f4 products straight on the codes in shared
 // memory, at the price of one bf16 product.  V's codes become f16 (exact) on
 // their way to the second product, since P needs more than e4m3's 4 bits.
 //
@@ -285,12 +287,16 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
-// P reaches 2^kQtTop where the maximum was last raised, and 2^(kQtTop +
-// kQtLazy) before it is raised again.  2^15 is the largest power of two in f16;
-// from 2^-17 of the largest P on, at worst, the smaller ones are rounded to
-// multiples of 2^-27 of it, which over 2^15 keys stays below the rounding of the
-// larger ones.  A raise stops the warpgroup for some 1000 cycles: with 6 and 8,
-// heads of large scores took 1.3 us a tile where others took 1.1.
+// P is an operand of the tensor cores beside V, so 16 bits: f16, since its 11
+// bits show in out and bf16's 8 would show eight times as much.  P reaches
+// 2^kQtTop where the maximum was last raised, and 2^(kQtTop + kQtLazy) before it
+// is raised again.  2^15 is the largest power of two in f16; below 2^-17 of the
+// largest P, at worst, the smaller ones are rounded to multiples of 2^-27 of it.
+// What n keys lose so is at most n 2^-28 of the largest: with 2^17 keys 2^-11, no
+// more than P's other rounding, with 2^20 keys 2^-8, as out's own (and only if
+// the errors all point one way).  A raise stops the warpgroup for some 1000
+// cycles: with 6 and 8, heads of large scores took 1.3 us a tile where others took
+// 1.1.  l is the sum of P before its rounding, in fp32: lse loses nothing.
 constexpr float kQtTop = 3.f, kQtLazy = 12.f;
 
 // l may be summed from P as long as no weight of consequence is 0 in P.  With

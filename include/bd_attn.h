@@ -513,6 +513,14 @@ BD_API bd_status bd_cache_read_q8(const void *k_cache, const void *v_cache,
  * NaN gives NaN.  Queries may be as small as bf16's smallest normal value; the
  * largest |q| |k| / sqrt(d) of a row has to fit fp32.
  *
+ * What is held in fewer than 32 bits on the way: a query value below 2^-10 of
+ * its row's largest is off by at most 2^-17 of that (none is where a kv-head's
+ * rows are few); the weights p that multiply V by 2^-11 of themselves, or, where
+ * p s (s: V's scale) is below 2^-17 of the row's largest such product, by 2^-28
+ * of that product, over s.  So out is off by at most 2^-11 sum p |v|, n 2^-28
+ * 448 max p s over n visible keys, and its rounding to bf16: for a million keys
+ * the second is 2^-8 of 448 max p s.  Sums and lse are fp32.
+ *
  * Errors: as bd_attn_decode and, for the cache, bd_cache_append_q8.
  */
 BD_API bd_status bd_attn_decode_q8(const void *q_blk, const void *k_cache,

@@ -8,7 +8,7 @@ import torch
 from oracle import serving
 import block_diffusion_lm_attn_b200 as bd
 from block_diffusion_lm_attn_b200 import build
-from test_gpu_serving import bits, f64, gen, i32, ok, randn, run_decode, verify_case
+from test_gpu_serving import bits, cuda_cache, f64, gen, i32, ok, randn, run_decode, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,31 @@ def test_decode_small_queries_over_large_keys(Hq, H, b, d, qe, ke):
     q = (randn(g, 1, Hq, b, d).float().clamp(-3, 3) * 2.0 ** qe).to(torch.bfloat16)
     q[:, 0] = (q[:, 0].float() * 2.0 ** -4).to(torch.bfloat16) if qe > -120 else q[:, 0]
     run_decode(q, ((kc, ks * 2.0 ** ke), v), lens, 0, 32)
+
+
+@pytest.mark.parametrize("Hq,H,b", [(4, 1, 1), (2, 1, 20)])
+@pytest.mark.parametrize("shift", [0.0, 0.3, 1.0])
+def test_decode_one_sharp_key_beside_a_quarter_of_a_million(Hq, H, b, shift):
+    """One key with about half the mass, the rest spread evenly over 2^18
+    others, whose weights are the smallest that f16 holds beside it: within the
+    bound of the header, n 2^-28 448 max p s beside the roundings of each key."""
+    d, group, n = 32, 128, 1 << 18
+    g = gen(5)
+    kc = torch.zeros((1, 1, n + 128, d), dtype=torch.uint8)
+    kc[0, 0, 0] = 0x38  # 1
+    vc = torch.randint(0x38, 0x7f, (1, 1, n + 128, d), generator=g).to(torch.uint8)
+    ks, vs = torch.ones(1, 1, (n + 128) // group), torch.full((1, 1, (n + 128) // group), 2.0 ** -8)
+    q = torch.full((1, Hq, b, d), (np.log(float(n)) + shift) / np.sqrt(d), dtype=torch.float32).to(torch.bfloat16)
+    lens = [n]
+    out, lse = bd.decode_q8(q.cuda(), cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 2, group)
+    ok()
+    k, v = (serving.values(c.numpy(), s.numpy(), group) for c, s in ((kc, ks), (vc, vs)))
+    ro, rl, mag, qk = serving.decode(f64(q), k, v, lens, 2)
+    p = np.exp(qk.max() / np.sqrt(d) - rl)  # the sharp key's weight
+    assert 0.4 < p.min() and p.max() < 0.8
+    # check_decode's bound, with the header's term for weights below f16's range
+    e = (qk * 2.0 ** -23 * (d + 8) + 2.0 ** -17 * np.sqrt(d) * np.abs(f64(q)).max(-1)) / np.sqrt(d)
+    tol = 2.0 ** -8 * np.abs(ro) + (e + 2.0 ** -11 + 2.0 ** -21)[..., None] * (mag + np.abs(ro))
+    tol = tol + (n * 2.0 ** -28 * 448 * 2.0 ** -8 * p)[..., None]
+    assert (np.abs(f64(out) - ro) <= tol).all()
+    assert (np.abs(f64(lse) - rl) <= e + 2.0 ** -20 * (1 + np.abs(rl)) + n * 2.0 ** -24).all()
