@@ -499,7 +499,8 @@ def rope_table(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
     ``device``, mscale).  ``scaling``: "plain", "linear" (positions divided by
     ``factor``), "ntk" (a larger base) or "yarn" (slow pairs divided by
     ``factor``, pairs that turn more than ``beta_fast`` times over
-    ``trained_len`` kept, and an attention factor ``mscale``)."""
+    ``trained_len`` kept, in between a ramp linear in the turns, and an
+    attention factor ``mscale``).  ``rope`` takes any other ``inv_freq`` too."""
     import torch
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be one of %s" % sorted(ROPE_SCALINGS))

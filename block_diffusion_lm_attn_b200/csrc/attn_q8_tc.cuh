@@ -709,39 +709,37 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     const int r8 = (lane & 4) ? (hrow ^ 5) : hrow;
                     const int u4 = lane & 3;
                     constexpr int H = DH <= 64 ? 1 : 2; // halves of 64 columns
-#pragma unroll 1
-                    for (int rr = 32 * cw; rr < 32 * cw + 32; rr += 32) {
-                        uint32_t x[4 * H][4]; // all loads go out first
+                    const int rr = 32 * cw; // this warp's rows
+                    uint32_t x[4 * H][4]; // all loads go out first
 #pragma unroll
-                        for (int i = 0; i < 4 * H; ++i) {
-                            const int r = rr + 8 * (i / H) + r8;
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
-                                         : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
-                                         : "memory");
-                        }
-                        if (ks + rr + 32 > hi) { // not keys: no code of theirs may be used
+                    for (int i = 0; i < 4 * H; ++i) {
+                        const int r = rr + 8 * (i / H) + r8;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
+                                     : "r"(src + r * 128 + ((((i % H) * 4 + u4) ^ r8) << 4))
+                                     : "memory");
+                    }
+                    if (ks + rr + 32 > hi) { // not keys: no code of theirs may be used
 #pragma unroll
-                            for (int i = 0; i < 4 * H; ++i)
-                                if (ks + rr + 8 * (i / H) + r8 >= hi)
-                                    x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
-                        }
+                        for (int i = 0; i < 4 * H; ++i)
+                            if (ks + rr + 8 * (i / H) + r8 >= hi)
+                                x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4 * H; ++i) {
-                            uint32_t y[8];
+                    for (int i = 0; i < 4 * H; ++i) {
+                        uint32_t y[8];
 #pragma unroll
-                            for (int t = 0; t < 8; ++t)
-                                y[t] = half2_of_e4m3x2((uint16_t)(x[i][t >> 1] >> (16 * (t & 1))));
-                            const uint32_t row = dst + (i % H) * kHalfTileBytes + (rr + 8 * (i / H) + r8) * 128;
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             row + (((2 * u4) ^ r8) << 4)),
-                                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                         : "memory");
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             row + (((2 * u4 + 1) ^ r8) << 4)),
-                                         "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                                         : "memory");
-                        }
+                        for (int t = 0; t < 8; ++t)
+                            y[t] = half2_of_e4m3x2((uint16_t)(x[i][t >> 1] >> (16 * (t & 1))));
+                        const uint32_t row = dst + (i % H) * kHalfTileBytes + (rr + 8 * (i / H) + r8) * 128;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         row + (((2 * u4) ^ r8) << 4)),
+                                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         row + (((2 * u4 + 1) ^ r8) << 4)),
+                                     "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                                     : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();

@@ -2,14 +2,14 @@
 // and kernel launches on the caller's stream.  See include/bd_attn.h for the
 // contract of each call.
 //
-// Kernels, all tcgen05 (head dims 64 and 32 on tiles zero-extended to 128
-// columns): the forward on the paired kernel (attn_tc_pair.cuh) when the GQA
+// Kernels, the attention ones on tcgen05 but for one (head dims 64 and 32 on
+// tiles zero-extended to 128 columns): the forward on the paired kernel (attn_tc_pair.cuh) when the GQA
 // group is even, else on the one-tile persistent kernel (attn_tc_persist.cuh),
 // which also runs block decode; the backward in attn_tc_bwd.cuh; the cache
 // and SPRINT kernels in cache_ops.cuh.  The serving step over a cache in 8
 // bits: rope.cuh (positions), cache_q8.cuh (writing and reading the cache),
-// attn_q8_tc.cuh and
-// attn_q8_rows.cuh (decode), spec_verify.cuh (verification).
+// attn_q8_tc.cuh (decode) and attn_q8_rows.cuh (decode for few query rows, the
+// one attention kernel on mma.sync), spec_verify.cuh (verification).
 #include "bd_attn.h"
 #include "bd_attn_debug.h"
 

@@ -399,6 +399,9 @@ BD_API size_t bd_sprint_workspace_bytes(int B, int S_cap);
  *                   (beta_fast - beta_slow) clamped to [0, 1], turns =
  *                   trained_len f_i / 2 pi (the "NTK-by-parts" rule of Peng et
  *                   al., "YaRN", section 3.2), and mscale = 0.1 ln(factor) + 1.
+ *                   The ramp w is linear in the turns, as in the paper.  Models
+ *                   trained with a ramp linear in the pair's index i, between two
+ *                   bounds, need a table of their own: bd_rope takes any inv_freq.
  *
  *   inv_freq  [rot_dim / 2] fp64, HOST memory (written)
  *   mscale    HOST memory (written): 1 but for BD_ROPE_YARN
