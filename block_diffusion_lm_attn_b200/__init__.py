@@ -491,6 +491,17 @@ def _launch(fn, dev, stream, args, tail=()):
     return fn(*args, handle, *tail)
 
 
+def _new(make, stream, *args, **kw):
+    """make(*args, **kw), an output that is made here, on the stream that the
+    call launches to: its memory then is that stream's, not what work queued on
+    the current one may still be using."""
+    if stream is None:
+        return make(*args, **kw)
+    import torch
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def rope_table(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
                factor: float = 1.0, trained_len: int = 0,
                beta_fast: float = 32.0, beta_slow: float = 1.0,
@@ -535,13 +546,13 @@ def rope(q, k, inv_freq, start=None, positions=None, period: int | None = None,
         Hkv = k.shape[1]
         _check_on(k, bf, (B, Hkv, N, d), dev, "k")
         if k_out is None:
-            k_out = torch.empty_like(k)
+            k_out = _new(torch.empty_like, stream, k)
         else:
             _check_on(k_out, bf, k.shape, dev, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _new(torch.empty_like, stream, q)
     else:
         _check_on(q_out, bf, q.shape, dev, "q_out")
     _check_on(inv_freq, torch.float64, (inv_freq.numel(),), dev, "inv_freq")
@@ -623,7 +634,7 @@ def cache_read_q8(k_cache, v_cache, k_scale, v_scale, cache_len, group: int,
     outs = []
     for t, w in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
-            t = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
+            t = _new(torch.zeros, stream, shape, dtype=torch.bfloat16, device=k_cache.device)
         else:
             _check_on(t, torch.bfloat16, shape, dev, w)
         outs.append(t)
@@ -649,11 +660,11 @@ def decode_q8(q_blk, k_cache, v_cache, k_scale, v_scale, cache_len, mode: int,
         raise ValueError("shape mismatch")
     _check_on(q_blk, torch.bfloat16, q_blk.shape, dev, "q_blk")
     if out is None:
-        out = torch.empty_like(q_blk)
+        out = _new(torch.empty_like, stream, q_blk)
     else:
         _check_on(out, torch.bfloat16, q_blk.shape, dev, "out")
     if lse is None:
-        lse = torch.empty((B, Hq, b), device=q_blk.device, dtype=torch.float32)
+        lse = _new(torch.empty, stream, (B, Hq, b), device=q_blk.device, dtype=torch.float32)
     else:
         _check_on(lse, torch.float32, (B, Hq, b), dev, "lse")
     ws_ptr, ws_bytes = None, 0
@@ -693,11 +704,11 @@ def spec_verify(draft, draft_prob, target_prob, u_accept, u_sample,
     if n_draft is not None:
         _check_on(n_draft, i32, (B,), dev, "n_draft")
     if n_accept is None:
-        n_accept = torch.empty(B, dtype=i32, device=draft.device)
+        n_accept = _new(torch.empty, stream, B, dtype=i32, device=draft.device)
     else:
         _check_on(n_accept, i32, (B,), dev, "n_accept")
     if next_token is None:
-        next_token = torch.empty(B, dtype=i32, device=draft.device)
+        next_token = _new(torch.empty, stream, B, dtype=i32, device=draft.device)
     else:
         _check_on(next_token, i32, (B,), dev, "next_token")
     st = _launch(load().bd_spec_verify, dev, stream, (

@@ -224,3 +224,36 @@ def test_verify_repeats_itself():
         again = bd.spec_verify(*args)
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
     ok()
+
+
+def test_outputs_made_on_the_stream_of_the_call():
+    """A call on a stream that is not the current one, which is busy: its
+    outputs neither wait for the current stream's queue (zeros among them) nor
+    lie in memory that the queue is still using."""
+    lens = [100, 60]
+    q, kv = decode_case(2, 8, 2, 3, 64, 128, 32, lens, 0, 5)
+    (kc, ks), (vc, vs) = kv
+    dev = (cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda())
+    q = q.cuda()
+    f, _ = bd.rope_table(64)
+    x, dp, tp, u, r = (t.cuda() for t in verify_case(2, 3, 90, 1)[:5])
+
+    def calls(stream):
+        return [*bd.rope(q, None, f, stream=stream)[:1], *bd.cache_read_q8(*dev, 32, stream=stream),
+                *bd.decode_q8(q, *dev, 0, 32, stream=stream), *bd.spec_verify(x, dp, tp, u, r, stream=stream)]
+
+    want = [t.clone() for t in calls(None)]
+    ok()
+    side = torch.cuda.Stream()
+    used = [torch.full_like(t, 3) for t in want for _ in range(4)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms of the current stream
+    copies = [t.clone() for t in used]
+    del used  # free for the current stream, whose copies are still to come
+    got = calls(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all((t == 3).all() for t in copies)
+    for a, c in zip(got, want):
+        assert torch.equal(a, c)
+    ok()
