@@ -273,6 +273,17 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
+def _new(make, stream, *args, **kw):
+    """make(*args, **kw), an output that is made here, on the stream that the
+    call launches to: its memory then is that stream's, not what work queued on
+    the current one may still be using."""
+    if stream is None:
+        return make(*args, **kw)
+    import torch
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def fwd(q, k, v, L: int, b: int, scale: float | None = None, out=None,
         lse=None, stream=None):
     """Training/prefill block-diffusion attention on CUDA tensors.
@@ -289,9 +300,9 @@ def fwd(q, k, v, L: int, b: int, scale: float | None = None, out=None,
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(torch.empty_like, stream, q)
     if lse is None:
-        lse = torch.empty((B, Hq, N), device=q.device, dtype=torch.float32)
+        lse = _new(torch.empty, stream, (B, Hq, N), device=q.device, dtype=torch.float32)
     st = bd_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                      lse.data_ptr(), B, Hq, Hkv, L, b, d, float(scale),
                      _stream_handle(stream))
@@ -316,12 +327,12 @@ def bwd(q, k, v, out, lse, dout, L: int, b: int, scale: float | None = None,
     _check(lse, torch.float32, "lse")
     if scale is None:
         scale = d ** -0.5
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new(torch.empty_like, stream, q) if dq is None else dq
+    dk = _new(torch.empty_like, stream, k) if dk is None else dk
+    dv = _new(torch.empty_like, stream, v) if dv is None else dv
     nb = bd_attn_bwd_workspace_bytes(B, Hq, L)
     if workspace is None:
-        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device)
+        workspace = _new(torch.empty, stream, nb, dtype=torch.uint8, device=q.device)
     st = bd_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                      lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
                      dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, L, b, d,
@@ -353,9 +364,9 @@ def decode(q_blk, k_cache, v_cache, cache_len, mode: int, out=None, lse=None,
         if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()):
             raise ValueError("q_blk and caches must be contiguous bf16 CUDA")
     if out is None:
-        out = torch.empty_like(q_blk)
+        out = _new(torch.empty_like, stream, q_blk)
     if lse is None:
-        lse = torch.empty((B, Hq, b), device=q_blk.device, dtype=torch.float32)
+        lse = _new(torch.empty, stream, (B, Hq, b), device=q_blk.device, dtype=torch.float32)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -384,7 +395,7 @@ def spec_accept(draft, target, n_accept=None, stream=None):
     if tuple(target.shape) != (B, b):
         raise ValueError("shape mismatch")
     if n_accept is None:
-        n_accept = torch.empty(B, dtype=torch.int32, device=draft.device)
+        n_accept = _new(torch.empty, stream, B, dtype=torch.int32, device=draft.device)
     st = bd_spec_accept(draft.data_ptr(), target.data_ptr(),
                         n_accept.data_ptr(), B, b, _stream_handle(stream))
     if st != BD_OK:
@@ -438,16 +449,16 @@ def sprint_prune(k_cache, v_cache, cache_len, conf, modality, alpha=0.5,
     _check(modality, torch.uint8, "modality")
     dev = k_cache.device
     if k_out is None:
-        k_out = torch.empty_like(k_cache)
+        k_out = _new(torch.empty_like, stream, k_cache)
     if v_out is None:
-        v_out = torch.empty_like(v_cache)
-    kept = torch.empty((B, S_cap), dtype=torch.int32, device=dev)
-    new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    score = (torch.zeros((B, S_cap), dtype=torch.float64, device=dev)
+        v_out = _new(torch.empty_like, stream, v_cache)
+    kept = _new(torch.empty, stream, (B, S_cap), dtype=torch.int32, device=dev)
+    new_len = _new(torch.empty, stream, B, dtype=torch.int32, device=dev)
+    score = (_new(torch.zeros, stream, (B, S_cap), dtype=torch.float64, device=dev)
              if want_score else None)
     nb = bd_sprint_workspace_bytes(B, S_cap)
     if workspace is None:
-        workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+        workspace = _new(torch.empty, stream, nb, dtype=torch.uint8, device=dev)
     st = bd_sprint_prune(k_cache.data_ptr(), v_cache.data_ptr(),
                          cache_len.data_ptr(), conf.data_ptr(),
                          modality.data_ptr(), float(alpha), float(keep_text),
@@ -489,17 +500,6 @@ def _launch(fn, dev, stream, args, tail=()):
     handle = (torch._C._cuda_getCurrentRawStream(dev) if stream is None
               else stream.cuda_stream)
     return fn(*args, handle, *tail)
-
-
-def _new(make, stream, *args, **kw):
-    """make(*args, **kw), an output that is made here, on the stream that the
-    call launches to: its memory then is that stream's, not what work queued on
-    the current one may still be using."""
-    if stream is None:
-        return make(*args, **kw)
-    import torch
-    with torch.cuda.stream(stream):
-        return make(*args, **kw)
 
 
 def rope_table(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
