@@ -432,7 +432,7 @@ inline bool supported_group(int T) { return T == 16 || T == 32 || T == 64 || T =
 // Query rows of a unit up to which the kernel for few rows takes it: 16 at a
 // time, and below d = 128 twice 16.  Measured over 24 prefixes of 4096 to 32768
 // keys, 8 kv-heads: 16 rows 148 us here, 190 us on the 128-row tiles (d = 128);
-// 17 to 32 rows 124 us and 172 us at d = 32, 153 us and 170 us at d = 64, 284 us
+// 17 to 32 rows 124 us and 172 us at d = 32, 158 us and 170 us at d = 64, 284 us
 // (registers spill) and 190 us at d = 128.
 constexpr int q8_few_rows(int d) { return d < 128 ? 32 : 16; }
 
