@@ -8,7 +8,7 @@ import torch
 from oracle import serving
 import block_diffusion_lm_attn_b200 as bd
 from block_diffusion_lm_attn_b200 import build
-from test_gpu_serving import bits, cuda_cache, f64, gen, i32, ok, randn, run_decode, verify_case
+from test_gpu_serving import bits, cuda_cache, decode_case, f64, gen, i32, ok, randn, run_decode, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -211,3 +211,57 @@ def test_decode_one_sharp_key_beside_a_quarter_of_a_million(Hq, H, b, shift):
     tol = tol + (n * 2.0 ** -28 * 448 * 2.0 ** -8 * p)[..., None]
     assert (np.abs(f64(out) - ro) <= tol).all()
     assert (np.abs(f64(lse) - rl) <= e + 2.0 ** -20 * (1 + np.abs(rl)) + n * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("Hq,H,b", ROWS)
+@pytest.mark.parametrize("grid", [0, 2, 7])
+def test_decode_far_scales_in_some_sequences(Hq, H, b, grid):
+    """V scales far apart in every other sequence, a prefix's first or last
+    groups alone: a CTA goes from segments of one kind to the other."""
+    B, d, group, S = 6, 64, 32, 1100
+    lens = [1000, 300, 64, 900, 1, 513]
+    q, kv = decode_case(B, Hq, H, b, d, S, group, lens, 1, 17)
+    (kc, ks), (vc, vs) = kv
+    vc[vc == 0] = 0x38  # (a code of 0 beside far larger values would ask for more than P holds)
+    vs[0, :, 0] = 2.0 ** -90
+    vs[2, :, :] = torch.exp2(torch.arange(vs.shape[2]).float() * 40 - 64)
+    vs[3, :, 20:] *= 2.0 ** 100
+    vs[5, 0, 15] = 2.0 ** -100
+    for i in range(B):  # no scale behind the visible rows
+        vs[i, :, -(-(lens[i] + b) // group):] = float("nan")
+    assert bd.bd_attn_debug_set_grid(grid) == bd.BD_OK
+    try:
+        run_decode(q, ((kc, ks), (vc, vs)), lens, 1, group)
+    finally:
+        bd.bd_attn_debug_set_grid(0)
+
+
+@pytest.mark.parametrize("Hq,H,b", ROWS)
+@pytest.mark.parametrize("grid", [0, 3])
+def test_decode_not_a_number_beside_far_scales(Hq, H, b, grid):
+    """NaN and infinite query rows give NaN rows, a NaN key NaN in the rows
+    that see it, no other row changes."""
+    g = gen(23)
+    lens = [700]
+    (kc, ks), (vc, vs) = far_scales(g, H, 900, 64, 32, -100, 100)
+    q = randn(g, 1, Hq, b, 64)
+    assert bd.bd_attn_debug_set_grid(grid) == bd.BD_OK
+    try:
+        def call(q, kc):
+            out, lse = bd.decode_q8(q.cuda(), cuda_cache(kc), cuda_cache(vc), ks.cuda(), vs.cuda(), i32(lens).cuda(), 1, 32)
+            ok()
+            return out.cpu(), lse.cpu()
+        good, lse_good = call(q, kc)
+        assert torch.isfinite(good).all() and torch.isfinite(lse_good).all()
+        q[0, 0, 0, 3], q[0, 1, b - 1, 0] = float("nan"), float("-inf")
+        kc = kc.clone()
+        kc[0, H - 1, 700 + b // 2, 5] = 0x7f  # seen by the rows from b // 2 on of the last kv-head
+        out, lse = call(q, kc)
+    finally:
+        bd.bd_attn_debug_set_grid(0)
+    want = torch.zeros((1, Hq, b), dtype=torch.bool)
+    want[0, 0, 0] = want[0, 1, b - 1] = True
+    want[0, Hq - Hq // H:, b // 2:] = True
+    assert torch.equal(torch.isnan(lse), want)
+    assert torch.equal(torch.isnan(out).all(-1), want) and torch.equal(torch.isnan(out).any(-1), want)
+    assert torch.equal(out[~want], good[~want]) and torch.equal(lse[~want], lse_good[~want])
