@@ -9,7 +9,8 @@
 // for any M; M follows max_j (x_j + log2 s_V(j)), so that P fits 11 bits.  Where
 // V's scales lie so far apart that a P beside M could be 0 in fp32 although its
 // key has weight (kQtSpread), l is summed from 2^(x_j - U) instead, U following
-// max_j x_j: more than one exponential a score, in a tile that no model has.
+// max_j x_j: a second exponential a score, in tiles that hardly a model has.
+// (Looking for them costs 0.7 us of the 79 below, calls in a row.)
 // A query row q = 2^e (hi + lo) is split into two e4m3 halves: hi rounds 2^-e q
 // to 4 significant bits, lo rounds the rest to 4 more, together the 8 of a bf16
 // for values from 2^-10 of the row's largest on; smaller ones are off by at most
